@@ -6,6 +6,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "prefill_plan.cuh"
 
 namespace gqla {
 cudaError_t launch_expand(const void *latent, int64_t num_slots, const void *w_uk,
@@ -36,6 +37,10 @@ cudaError_t launch_combine(const gqla_kv_index *kv, int s_q, int num_splits, int
                            int d_in, const float *o_part, const float *lse_part, const void *w_uv,
                            void *out, float *lse_out, int heads, int num_groups, bool skip_single,
                            cudaStream_t stream);
+cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_starts, int heads, int num_groups,
+                               const void *kv, const void *k_rope, int64_t num_slots, const gqla_kv_index *idx,
+                               int num_splits, float scale, float *o_part, float *lse_part, void *out,
+                               float *lse_out, void *ws, cudaStream_t stream);
 int group_splits_rule(int num_splits, int num_groups, int sms);
 extern thread_local int g_drop_v_unit;
 }  // namespace gqla
@@ -71,6 +76,17 @@ int check_index(const gqla_kv_index *kv) {
         return GQLA_ERR_INVALID_ARG;
     if (kv->batch > 65535) return GQLA_ERR_UNSUPPORTED;
     if (kv->page_size != kPage) return GQLA_ERR_UNSUPPORTED;
+    return GQLA_OK;
+}
+
+// Dimensions of the calls on ragged batches of new tokens: any number of groups, 1 to 128
+// heads in each (the heads of a group and its tokens share a 128-row tile).
+int check_ragged_dims(const gqla_dims *d) {
+    if (!d) return GQLA_ERR_INVALID_ARG;
+    if (d->num_heads <= 0 || d->num_groups <= 0 || d->num_heads % d->num_groups) return GQLA_ERR_INVALID_ARG;
+    if (!(d->softmax_scale > 0.0f) || !isfinite(d->softmax_scale)) return GQLA_ERR_INVALID_ARG;
+    if (!dims_supported(d)) return GQLA_ERR_UNSUPPORTED;
+    if (d->num_heads / d->num_groups > kPfRows) return GQLA_ERR_UNSUPPORTED;
     return GQLA_OK;
 }
 
@@ -438,6 +454,50 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
     return cuda_status(launch_combine(kv, s_q, num_splits, lead_splits, lead_weight16, d_in, o_part,
                                       lse_part, w_uv, out, lse_out, dims->num_heads, dims->num_groups,
                                       false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gqla_prefill_slots(int num_splits) {
+    if (num_splits <= 0 || num_splits > 65535) return GQLA_ERR_INVALID_ARG;
+    return 2 * num_splits;
+}
+
+int gqla_plan_prefill(const gqla_dims *dims, const int32_t *new_tokens, const int32_t *seqlens, int batch,
+                      int max_splits) {
+    const int st = check_ragged_dims(dims);
+    if (st != GQLA_OK) return st;
+    if (!new_tokens || !seqlens || batch <= 0 || batch > 65535 || max_splits <= 0 || max_splits > 65535)
+        return GQLA_ERR_INVALID_ARG;
+    const int W = pf_block_tokens(dims->num_heads / dims->num_groups);
+    int64_t total = 0;
+    for (int b = 0; b < batch; ++b) {
+        if (new_tokens[b] < 0 || seqlens[b] < new_tokens[b]) return GQLA_ERR_INVALID_ARG;
+        if (new_tokens[b] > 0)
+            total += dims->num_groups * pf_tiles_before(new_tokens[b], seqlens[b], W, pf_blocks(new_tokens[b], W));
+    }
+    return (int)std::max<int64_t>(1, std::min<int64_t>(max_splits, total));
+}
+
+int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, const int32_t *q_starts,
+                     const void *kv_expanded, const void *k_rope, int64_t num_slots, const gqla_kv_index *kv,
+                     int num_splits, float *o_part, float *lse_part, void *out, float *lse_out,
+                     void *workspace, size_t workspace_bytes, gqla_stream_t stream) {
+    int st = check_ragged_dims(dims);
+    if (st != GQLA_OK) return st;
+    if ((st = check_index(kv)) != GQLA_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
+    if (total_q < 0 || num_splits <= 0 || num_splits > 65535) return GQLA_ERR_INVALID_ARG;
+    if (!q || !q_starts || !kv_expanded || !k_rope || !out) return GQLA_ERR_INVALID_ARG;
+    if (num_splits > 1 && (!o_part || !lse_part)) return GQLA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kv_expanded) || !aligned16(k_rope) || !aligned16(out) ||
+        (o_part && !aligned16(o_part)))
+        return GQLA_ERR_INVALID_ARG;
+    if (num_slots != (int64_t)kv->num_pages * kv->page_size) return GQLA_ERR_INVALID_ARG;
+    const int64_t most = ((int64_t)1 << 31) - 1;
+    if (total_q > most || num_slots > most) return GQLA_ERR_UNSUPPORTED;
+    if (total_q == 0) return GQLA_OK;
+    return cuda_status(launch_prefill_gqa(q, total_q, q_starts, dims->num_heads, dims->num_groups, kv_expanded,
+                                          k_rope, num_slots, kv, num_splits, dims->softmax_scale, o_part, lse_part,
+                                          out, lse_out, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,786 @@
+// prefill.cu -- attention of chunks of new tokens over the paged expanded cache (GQA
+// path): every new token of a sequence attends to the cached tokens up to and including
+// itself, G query heads sharing each group's [K_nope | k^R] and V (GQLA, paperlayer.ai
+// summary, sec. 3 "Two equivalent decoding paths": the g K/V groups are materialised and
+// attention over them is standard grouped-query attention).
+//
+// Bound by the tensor cores for chunks (2 (192 + 128) FLOPs per visible (row, key) pair
+// against 640 bytes per key shared by 256 rows) and by HBM when a few rows meet a long
+// context.
+//
+//  * A query block is 256 rows: two MMA tiles of 128 rows = (128 / G) tokens x G heads of
+//    one group, so the heads of a group share every key tile on chip. Per key tile of 128
+//    tokens (two pages) and MMA tile:
+//      S[128 x 128]   = q (128 x 192, smem) x K^T (192 x 128, smem)
+//      O[128 x 128]  += P (128 x 128, bf16 in TMEM over S) x V (128 x 128, smem, MN-major)
+//    S0, S1, O0, O1 take the 512 TMEM columns. While one tile's softmax runs, the other
+//    tile's products do.
+//  * 12 warps: warp 0 TMA producer, warp 1 MMA issuer, warp 2 TMEM owner, warp 3 clears V
+//    rows past a block's last key; warps 4-7 and 8-11 the softmax of tile 0 and tile 1, one
+//    query row per thread (no exchange between threads), fp32 online softmax in the base-2
+//    domain with lazy rescaling (O is touched only when a row's maximum rises by more than
+//    2^8).
+//  * K and V pass through one ring of eight 16 KB units (K: 64 columns x 128 keys, three to
+//    a tile; V: 64 keys x 128 columns, two to a tile), in the order of use.
+//  * Work split: prefill_plan.cuh. Every CTA derives its chunk from the device-resident
+//    lengths.
+//  * Every wait is bounded; a wait that runs out records GQLA_ERR_TIMEOUT and the CTA
+//    drains and exits.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "prefill_plan.cuh"
+#include "sm100.cuh"
+#include "tensor_map.cuh"
+
+namespace gqla {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kPfThreads = 384;
+constexpr int kPfLaunchRegs = 168;
+constexpr int kPfIssueRegs = 72, kPfSoftmaxRegs = 216;
+static_assert(128 * kPfIssueRegs + 256 * kPfSoftmaxRegs <= kPfThreads * kPfLaunchRegs, "register split");
+constexpr float kPfRescaleLog2 = 8.0f;
+
+constexpr int kPfBox = 64 * 128;          // one TMA box: 64 rows of 128 bytes
+constexpr int kPfUnit = 2 * kPfBox;       // ring unit
+constexpr int kPfUnits = 8;               // units in the ring
+constexpr int kPfQBlock = kPfRows * 128;  // 64 columns of a query tile
+
+struct PfSmem {
+    static constexpr int oQ = 0;                                   // [2 tiles][3 column blocks]
+    static constexpr int oRing = oQ + 6 * kPfQBlock;
+    static constexpr int oBar = oRing + kPfUnits * kPfUnit;
+    // full/empty[units], q_full/q_empty[2], s_full[2], p_full[2], o_full/o_free[2], v_ask,
+    // v_fixed, drain
+    static constexpr int kNumBars = 2 * kPfUnits + 4 + 2 + 2 + 4 + 2 + 1;
+    static constexpr int oPlan = oBar + kNumBars * 8;              // int64 rem; int b, g, i, t
+    static constexpr int oMisc = oPlan + 32;                       // tmem base, abort flag
+    static constexpr int kBytes = oMisc + 16;
+    static constexpr int kAlloc = kBytes + 1024;
+};
+static_assert(PfSmem::kAlloc <= 227 * 1024, "shared memory");
+
+struct PfParams {
+    const int32_t *q_starts;
+    const int32_t *page_table;
+    const int32_t *seqlens;
+    float *o_part;    // [2 num_splits][256][128]
+    float *lse_part;  // [2 num_splits][256]
+    __nv_bfloat16 *out;
+    float *lse_out;
+    void *ws;
+    int64_t total_q;
+    int64_t num_slots;
+    int batch, max_pages, num_pages, num_splits, heads, groups, G, tile_tokens, block_tokens;
+    float scale_log2;
+};
+
+// Bounded wait of a role that may have nothing to do for whole blocks (a query tile that
+// short blocks leave empty, the V rows of blocks that end on a tile): the roles that feed it
+// give up after kWaitCycles and raise the abort flag; its own limit is 32 times that.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (clock64() - t0 > 32 * kWaitCycles) return false;
+    }
+}
+
+// New tokens n, cached tokens L and first query row of a sequence; n = 0 for a sequence
+// without new tokens and for one whose numbers are inconsistent (reported by `bad`).
+struct PfSeq {
+    int n, L;
+    int64_t q0;
+    bool bad;
+};
+
+__device__ __forceinline__ PfSeq pf_seq(const PfParams &p, int b) {
+    const int a = p.q_starts[b], e = p.q_starts[b + 1], L = p.seqlens[b];
+    PfSeq s;
+    s.bad = a < 0 || e < a || (int64_t)e > p.total_q || (e > a && L < e - a) ||
+            (int64_t)L > (int64_t)p.max_pages * kPage;
+    s.n = s.bad ? 0 : e - a;
+    s.L = L;
+    s.q0 = a;
+    return s;
+}
+
+__device__ __forceinline__ int64_t pf_seq_tiles(const PfParams &p, const PfSeq &s) {
+    return s.n > 0 ? p.groups * pf_tiles_before(s.n, s.L, p.block_tokens, pf_blocks(s.n, p.block_tokens)) : 0;
+}
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ int64_t warp_scan64(int64_t v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t n = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += n;
+    }
+    return v;
+}
+
+// One full warp: the batch's (block, tile) pairs; sequences with bad numbers are reported
+// when `report`.
+__device__ int64_t pf_total(const PfParams &p, bool report) {
+    int64_t acc = 0;
+    for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
+        const PfSeq s = pf_seq(p, b);
+        if (s.bad && report) report_error(p.ws, GQLA_ERR_DEVICE, b);
+        acc += pf_seq_tiles(p, s);
+    }
+    return warp_sum64(acc);
+}
+
+// A place in the plan: sequence, group, block, tile, and (block_start) the position of the
+// block's first pair.
+struct PfPlace {
+    int b, g, i, t;
+    int64_t block_start;
+};
+
+// One full warp: the place of pair `pos` (0 <= pos < total).
+__device__ PfPlace pf_find(const PfParams &p, int64_t pos) {
+    const int lane = threadIdx.x & 31;
+    PfPlace r{p.batch, 0, 0, 0, 0};
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        PfSeq s{0, 0, 0, false};
+        if (b < p.batch) s = pf_seq(p, b);
+        const int64_t mine = pf_seq_tiles(p, s);
+        const int64_t incl = warp_scan64(mine);
+        const unsigned hit = __ballot_sync(0xffffffffu, mine > 0 && base + incl > pos);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            const int64_t start = base + __shfl_sync(0xffffffffu, incl - mine, src);
+            const int n = __shfl_sync(0xffffffffu, s.n, src), L = __shfl_sync(0xffffffffu, s.L, src);
+            const int W = p.block_tokens, m = pf_blocks(n, W);
+            const int64_t per_group = pf_tiles_before(n, L, W, m);
+            int64_t off = pos - start;
+            r.b = b0 + src;
+            r.g = (int)(off / per_group);
+            off -= r.g * per_group;
+            // the block whose pairs hold `off`: the last i with tiles_before(i) <= off
+            int lo = 0, hi = m;  // tiles_before(lo) <= off < tiles_before(hi)
+            while (hi - lo > 1) {
+                const int step = (hi - lo + 31) / 32;
+                const int c = lo + (lane + 1) * step;
+                const bool le = c < hi && pf_tiles_before(n, L, W, c) <= off;
+                const int k = __popc(__ballot_sync(0xffffffffu, le));
+                hi = min(hi, lo + (k + 1) * step);
+                lo += k * step;
+            }
+            r.i = lo;
+            const int64_t before = pf_tiles_before(n, L, W, lo);
+            r.t = (int)(off - before);
+            r.block_start = pos - r.t;
+            return r;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return r;
+}
+
+// One piece: key tiles [t0, t1) of a query block.
+struct PfPiece {
+    int b, g;
+    int64_t row0;   // query row (token) of the block's first token
+    int ntok;       // its tokens
+    int pos0;       // the first token's position in the sequence
+    int t0, t1;     // key tiles of this chunk
+    int nt;         // key tiles of the block
+    int kv_end;     // keys of the block
+};
+
+// Walks the pieces of a chunk; the same in every role.
+struct PfIter {
+    PfSeq s;
+    int b, g, i, t;
+    int64_t rem;
+    bool started;
+    __device__ __forceinline__ PfIter(const PfParams &p, const int *plan) {
+        rem = *reinterpret_cast<const int64_t *>(plan);
+        b = plan[2];
+        g = plan[3];
+        i = plan[4];
+        t = plan[5];
+        started = false;
+        if (rem > 0 && b < p.batch) s = pf_seq(p, b);
+    }
+    __device__ __forceinline__ bool next(const PfParams &p, PfPiece &o) {
+        if (rem <= 0) return false;
+        if (started) {
+            t = 0;
+            if (++i * p.block_tokens >= s.n) {
+                i = 0;
+                if (++g == p.groups) {
+                    g = 0;
+                    do {
+                        ++b;
+                        if (b < p.batch) s = pf_seq(p, b);
+                    } while (b < p.batch && s.n == 0);
+                }
+            }
+        }
+        started = true;
+        if (b >= p.batch) return false;
+        const int first = i * p.block_tokens;
+        o.b = b;
+        o.g = g;
+        o.row0 = s.q0 + first;
+        o.ntok = min(p.block_tokens, s.n - first);
+        o.pos0 = s.L - s.n + first;
+        o.kv_end = o.pos0 + o.ntok;
+        o.nt = (o.kv_end + kPfTile - 1) / kPfTile;
+        o.t0 = t;
+        o.t1 = (int)min((int64_t)o.nt, t + rem);
+        rem -= o.t1 - o.t0;
+        return true;
+    }
+};
+
+// Ring units: K(s) is three units and precedes V(s - 1), two units, in the order of use
+// (S of step s + 1 is issued before O of step s needs V(s)); V of the last step ends it.
+__device__ __forceinline__ uint32_t k_unit(uint32_t s) { return s == 0 ? 0 : 5 * s - 2; }
+__device__ __forceinline__ uint32_t v_unit(uint32_t s, uint32_t steps) {
+    return s + 1 < steps ? 5 * s + 6 : 5 * s + 3;
+}
+
+__global__ void __launch_bounds__(kPfThreads, 1)
+    prefill_gqa_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap kr_map,
+                       const __grid_constant__ CUtensorMap q_map, const PfParams p) {
+    using SM = PfSmem;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + SM::oBar), *empty = full + kPfUnits;
+    uint64_t *q_full = empty + kPfUnits, *q_empty = q_full + 2;
+    uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *o_free = o_full + 2;
+    uint64_t *v_ask = o_free + 2, *v_fixed = v_ask + 1, *drain = v_fixed + 1;
+    int *plan = reinterpret_cast<int *>(smem + SM::oPlan);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::oMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::oMisc + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPfUnits; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
+            mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1); mbar_init(&o_free[i], 4);
+        }
+        mbar_init(v_ask, 1);
+        mbar_init(v_fixed, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&kv_map);
+        prefetch_tensormap(&kr_map);
+        prefetch_tensormap(&q_map);
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    if (warp == 0) {
+        const int64_t total = pf_total(p, c == 0);
+        const int64_t k = (total + p.num_splits - 1) / p.num_splits;
+        const int64_t r0 = c * k, rem = min(total, r0 + k) - r0;
+        PfPlace at{0, 0, 0, 0, 0};
+        if (rem > 0) at = pf_find(p, r0);
+        if (lane == 0) {
+            *reinterpret_cast<int64_t *>(plan) = rem > 0 ? rem : 0;
+            plan[2] = at.b; plan[3] = at.g; plan[4] = at.i; plan[5] = at.t;
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t steps = (uint32_t)*reinterpret_cast<const int64_t *>(plan);
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfIssueRegs));
+        if (warp == 0) {
+            // ------------------------------------------------------------ TMA producer
+            if (lane == 0 && steps > 0) {
+                uint32_t u = 0, qn[2] = {0, 0};
+                auto unit = [&]() -> uint8_t * {  // the next ring unit, once it is free
+                    const uint32_t sl = u % kPfUnits;
+                    if (!mbar_wait(&empty[sl], ((u / kPfUnits) & 1) ^ 1, abort_flag)) *abort_flag = 1;
+                    if (*abort_flag) return nullptr;
+                    mbar_arrive_expect_tx(&full[sl], kPfUnit);
+                    return smem + SM::oRing + sl * kPfUnit;
+                };
+                // first cache slot of the pages of a tile; a missing page reads as zeros
+                // (a row past the end of the map)
+                struct Slots { int s0, s1; };
+                auto slots = [&](const PfPiece &pc, int t) -> Slots {
+                    const int32_t *row = p.page_table + (int64_t)pc.b * p.max_pages;
+                    const int pg = 2 * t, pages = (pc.kv_end + kPage - 1) / kPage;
+                    const int a0 = row[pg], a1 = pg + 1 < pages ? row[pg + 1] : 0;
+                    const bool ok0 = a0 >= 0 && a0 < p.num_pages, ok1 = a1 >= 0 && a1 < p.num_pages;
+                    if (!ok0 || !ok1) report_error(p.ws, GQLA_ERR_DEVICE, pc.b);
+                    return Slots{ok0 ? a0 * kPage : (int)p.num_slots,
+                                 ok1 && pg + 1 < pages ? a1 * kPage : (int)p.num_slots};
+                };
+                auto load_v = [&](int g, const Slots &sl) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint8_t *dst = unit();
+                        if (!dst) return;
+                        uint64_t *bar = &full[u % kPfUnits];
+                        const int y = h ? sl.s1 : sl.s0;
+                        tma_load_3d(dst, &kv_map, bar, kNope, y, g);
+                        tma_load_3d(dst + kPfBox, &kv_map, bar, kNope + 64, y, g);
+                        ++u;
+                    }
+                };
+                PfIter it(p, plan);
+                PfPiece pc;
+                Slots prev{0, 0};
+                int prev_g = -1;
+                const uint32_t q_bytes = (uint32_t)(p.tile_tokens * p.G) * 128u;
+                while (!*abort_flag && it.next(p, pc)) {
+                    for (int q = 0; q < 2 && q * p.tile_tokens < pc.ntok; ++q) {
+                        if (!mbar_wait(&q_empty[q], (qn[q] & 1) ^ 1, abort_flag)) *abort_flag = 1;
+                        if (*abort_flag) break;
+                        ++qn[q];
+                        mbar_arrive_expect_tx(&q_full[q], 3 * q_bytes);
+                        for (int cb = 0; cb < 3; ++cb)
+                            tma_load_3d(smem + SM::oQ + (3 * q + cb) * kPfQBlock, &q_map, &q_full[q], 64 * cb,
+                                        pc.g * p.G, (int)(pc.row0 + q * p.tile_tokens));
+                    }
+                    for (int t = pc.t0; t < pc.t1 && !*abort_flag; ++t) {
+                        const Slots sl = slots(pc, t);
+#pragma unroll
+                        for (int cb = 0; cb < 3; ++cb) {  // K_nope lo, hi, RoPE keys: 64 columns x 128 keys
+                            uint8_t *dst = unit();
+                            if (!dst) break;
+                            uint64_t *bar = &full[u % kPfUnits];
+                            if (cb < 2) {
+                                tma_load_3d(dst, &kv_map, bar, 64 * cb, sl.s0, pc.g);
+                                tma_load_3d(dst + kPfBox, &kv_map, bar, 64 * cb, sl.s1, pc.g);
+                            } else {
+                                tma_load_2d(dst, &kr_map, bar, 0, sl.s0);
+                                tma_load_2d(dst + kPfBox, &kr_map, bar, 0, sl.s1);
+                            }
+                            ++u;
+                        }
+                        if (prev_g >= 0) load_v(prev_g, prev);
+                        prev = sl;
+                        prev_g = pc.g;
+                    }
+                }
+                if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev);
+                // never leave with copies in flight: wait (bounded) for the last ones issued
+                int dummy = 0;
+                volatile int *no_abort = reinterpret_cast<volatile int *>(&dummy);
+                for (uint32_t x = (u > kPfUnits ? u - kPfUnits : 0); x < u; ++x)
+                    mbar_wait(&full[x % kPfUnits], (x / kPfUnits) & 1, no_abort);
+                for (int q = 0; q < 2; ++q)
+                    if (qn[q]) mbar_wait(&q_full[q], (qn[q] - 1) & 1, no_abort);
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0 && steps > 0) {
+                constexpr uint32_t idesc_s = idesc_bf16(kPfRows, kPfTile, 0, 0);
+                constexpr uint32_t idesc_pv = idesc_bf16(kPfRows, kDv, 0, 1);
+                const uint64_t q_d0 = smem_desc(smem_u32(smem + SM::oQ), 16, 1024, kSw128);
+                const uint64_t k_d0 = smem_desc(smem_u32(smem + SM::oRing), 16, 1024, kSw128);
+                const uint64_t v_d0 = smem_desc(smem_u32(smem + SM::oRing), kPfBox, 1024, kSw128);
+                uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0}, fixes = 0;
+                auto wait = [&](uint64_t *bar, uint32_t parity) {
+                    if (!mbar_wait(bar, parity, abort_flag)) *abort_flag = 1;
+                };
+                // S_q of step s; the step's last query tile frees the K units, a piece's last step
+                // the query tile
+                auto score = [&](const PfPiece &pc, int t, uint32_t s, int q, int nq) {
+                    if (t == pc.t0) wait(&q_full[q], qn[q]++ & 1);
+                    const uint32_t u = k_unit(s);
+#pragma unroll
+                    for (int cb = 0; cb < 3; ++cb) {
+                        const uint32_t sl = (u + cb) % kPfUnits;
+                        if (q == 0) wait(&full[sl], ((u + cb) / kPfUnits) & 1);
+                        tc_fence_after();
+                        if (!*abort_flag) {
+                            const uint64_t qd = desc_advance(q_d0, (3 * q + cb) * kPfQBlock);
+                            const uint64_t kd = desc_advance(k_d0, sl * kPfUnit);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_bf16(tmem + kPfTile * q, desc_advance(qd, ks * 32), desc_advance(kd, ks * 32),
+                                         idesc_s, (cb > 0 || ks > 0) ? 1u : 0u);
+                        }
+                        if (q == nq - 1) mma_commit(&empty[sl]);
+                    }
+                    mma_commit(&s_full[q]);
+                    if (t == pc.t1 - 1) mma_commit(&q_empty[q]);
+                };
+                // O_q of step s
+                auto product = [&](const PfPiece &pc, int t, uint32_t s, int q, int nq) {
+                    const uint32_t u = v_unit(s, steps);
+                    if (q == 0) {
+                        for (int h = 0; h < 2; ++h) wait(&full[(u + h) % kPfUnits], ((u + h) / kPfUnits) & 1);
+                        if (t == pc.nt - 1 && pc.kv_end % kPfTile != 0) {
+                            mbar_arrive(v_ask);
+                            wait(v_fixed, fixes++ & 1);
+                        }
+                    }
+                    if (t == pc.t0) wait(&o_free[q], (on[q]++ & 1) ^ 1);
+                    wait(&p_full[q], pn[q]++ & 1);
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t sl = (u + h) % kPfUnits;
+                        if (!*abort_flag) {
+                            const uint64_t vd = desc_advance(v_d0, sl * kPfUnit);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_bf16_ts(tmem + 256 + kDv * q, tmem + kPfTile * q + 32 * h + 8 * ks,
+                                            desc_advance(vd, ks * 2048), idesc_pv,
+                                            (t > pc.t0 || h > 0 || ks > 0) ? 1u : 0u);
+                        }
+                        if (q == nq - 1) mma_commit(&empty[sl]);
+                    }
+                    if (t == pc.t1 - 1) mma_commit(&o_full[q]);
+                };
+                PfIter it(p, plan);
+                PfPiece pc, nx;
+                it.next(p, pc);
+                int t = pc.t0, nq = pc.ntok > p.tile_tokens ? 2 : 1;
+                for (int q = 0; q < nq; ++q) score(pc, t, 0, q, nq);
+                for (uint32_t s = 0; s < steps && !*abort_flag; ++s) {
+                    // the step after this one
+                    nx = pc;
+                    int nt = t + 1, nnq = nq;
+                    bool more = true;
+                    if (nt == pc.t1) {
+                        more = it.next(p, nx);
+                        nt = nx.t0;
+                        nnq = nx.ntok > p.tile_tokens ? 2 : 1;
+                    }
+                    for (int q = 0; q < 2; ++q) {
+                        if (q < nq) product(pc, t, s, q, nq);
+                        if (more && q < nnq) score(nx, nt, s + 1, q, nnq);
+                    }
+                    pc = nx;
+                    t = nt;
+                    nq = nnq;
+                }
+                // nothing may still be running when TMEM is freed
+                mma_commit(drain);
+                int dummy = 0;
+                mbar_wait(drain, 0, reinterpret_cast<volatile int *>(&dummy));
+            }
+        } else if (warp == 3) {
+            // ------------------------------------------------------------ V rows past the keys
+            // The last tile of a block ends at its last query token, rarely at the tile's end:
+            // the rows past it (later tokens, or slots that hold no token and may hold NaN) meet
+            // P = 0 in the product and are cleared so that 0 x NaN cannot enter it.
+            // The MMA issuer asks for it once V has landed and waits until it is done.
+            PfIter it(p, plan);
+            PfPiece pc;
+            uint32_t s = 0, fixes = 0;
+            while (it.next(p, pc)) {
+                s += pc.t1 - pc.t0;
+                const int keep = pc.kv_end % kPfTile;
+                if (pc.t1 != pc.nt || keep == 0) continue;
+                const uint32_t u = v_unit(s - 1, steps);
+                bool ok = mbar_wait_long(v_ask, fixes++ & 1, abort_flag);
+                for (int h = 0; h < 2; ++h)
+                    ok = ok && mbar_wait(&full[(u + h) % kPfUnits], ((u + h) / kPfUnits) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t sl = (u + h) % kPfUnits;
+                    uint8_t *v = smem + SM::oRing + sl * kPfUnit;
+                    const int r0 = min(max(keep - kPage * h, 0), kPage);  // first row to clear in this page
+                    for (int i = lane; i < (kPage - r0) * 16; i += 32)
+                        *reinterpret_cast<uint4 *>(v + (i & 1) * kPfBox + (r0 + (i >> 4)) * 128 + ((i >> 1) & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_fixed);
+            }
+        }
+        // warp 2 owns TMEM and is otherwise idle
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfSoftmaxRegs));
+        // ---------------------------------------------------------------- softmax, epilogue
+        const int q = (warp - 4) >> 2;             // query tile
+        const int row = 32 * (warp & 3) + lane;    // this thread's query row: its TMEM lane
+        const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t t_s = tmem + kPfTile * q + lane_off, t_o = tmem + 256 + kDv * q + lane_off;
+        const int tok = q * p.tile_tokens + row / p.G, hg = row % p.G;  // token of the block, head of the group
+        const bool in_tile = row < p.tile_tokens * p.G;
+        uint32_t sn = 0, on = 0;
+        PfIter it(p, plan);
+        PfPiece pc;
+        bool alive = true;  // the same in all lanes of the warp
+        while (alive && it.next(p, pc)) {
+            if (q * p.tile_tokens >= pc.ntok) continue;
+            const bool valid = in_tile && tok < pc.ntok;
+            const bool warp_valid = __any_sync(0xffffffffu, valid);
+            const int last = pc.pos0 + tok;   // the last key this row sees
+            float m = -INFINITY, l = 0.0f;    // maximum (log2 units) and sum of this row
+            for (int t = pc.t0; t < pc.t1; ++t) {
+                alive = __all_sync(0xffffffffu, mbar_wait_long(&s_full[q], sn++ & 1, abort_flag));
+                if (!alive) break;
+                tc_fence_after();
+                if (warp_valid) {
+                    uint32_t sv[128];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32 * i, sv + 32 * i);
+                    tmem_wait_ld();
+                    const int lim = valid ? last + 1 - t * kPfTile : 0;  // keys of this tile that the row sees
+                    if (__any_sync(0xffffffffu, lim < kPfTile)) {
+#pragma unroll
+                        for (int e = 0; e < 128; ++e)
+                            if (e >= lim) sv[e] = 0xff800000u;
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[e]));
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                    // S of this step complete means O of the step before is: they are issued in order
+                    const bool rise = mt > m + kPfRescaleLog2;
+                    if (__any_sync(0xffffffffu, rise)) {
+                        const float a = rise ? fast_exp2(m - mt) : 1.0f;  // 0 from an empty row
+                        if (rise) m = mt;
+                        l *= a;
+                        if (t > pc.t0) {
+#pragma unroll 1
+                            for (int i = 0; i < kDv; i += 16) {
+                                uint32_t r[16];
+                                tmem_ld16(t_o + i, r);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * a);
+                                tmem_st16(t_o + i, r);
+                            }
+                        }
+                    }
+                    const float mu = m == -INFINITY ? 0.0f : m;
+                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 128; i += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float p0 = fast_exp2(fmaf(__uint_as_float(sv[i + e]), p.scale_log2, -mu));
+                            const float p1 = fast_exp2(fmaf(__uint_as_float(sv[i + e + 1]), p.scale_log2, -mu));
+                            ls[e & 2] += p0;
+                            ls[(e & 2) + 1] += p1;
+                            __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+                            w[e / 2] = *reinterpret_cast<uint32_t *>(&h2);
+                        }
+                        tmem_st16(t_s + i / 2, w);
+                    }
+                    l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[q]);
+            }
+            // ---- epilogue: O / l and the LSE, to the output or to this piece's partial
+            alive = alive && __all_sync(0xffffffffu, mbar_wait(&o_full[q], on++ & 1, abort_flag));
+            if (!alive) break;
+            tc_fence_after();
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const float lse = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
+            const int64_t prow = (int64_t)(2 * c + (pc.t0 == 0 ? 1 : 0)) * kPfBlockRows + q * kPfRows + row;
+            const int64_t orow = (pc.row0 + tok) * p.heads + pc.g * p.G + hg;
+            if (warp_valid) {
+                if (valid) {
+                    if (!whole) p.lse_part[prow] = lse;
+                    else if (p.lse_out) p.lse_out[orow] = lse;
+                }
+#pragma unroll
+                for (int i = 0; i < kDv; i += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(t_o + i, r);
+                    tmem_wait_ld();
+                    if (!valid) continue;
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * kDv + i);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            const uint2 a = pack_bf16x4(__uint_as_float(r[e]) * inv, __uint_as_float(r[e + 1]) * inv,
+                                                        __uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
+                            const uint2 b = pack_bf16x4(__uint_as_float(r[e + 4]) * inv, __uint_as_float(r[e + 5]) * inv,
+                                                        __uint_as_float(r[e + 6]) * inv, __uint_as_float(r[e + 7]) * inv);
+                            dst[e / 8] = make_uint4(a.x, a.y, b.x, b.y);
+                        }
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.o_part + prow * kDv + i);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            dst[e / 4] = make_float4(__uint_as_float(r[e]) * inv, __uint_as_float(r[e + 1]) * inv,
+                                                     __uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[q]);
+        }
+        if (!alive) *abort_flag = 1;
+    }
+
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) report_error(p.ws, GQLA_ERR_TIMEOUT, c);
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Merge of the cut blocks. CTA (c - 1, y) looks at the boundary between the chunks c - 1
+// and c: if it is the first one inside its block (the block begins in chunk c - 1), the
+// CTA merges the block's pieces, slots 2 (c - 1) + 1, 2 c, 2 (c + 1), ... up to the chunk
+// that holds its last pair, for the rows 32 y .. 32 y + 31. One warp per row, four columns
+// a lane, partials in chunk order.
+// ---------------------------------------------------------------------------
+constexpr int kPcRows = 32, kPcWarps = 8;
+
+__global__ void __launch_bounds__(32 * kPcWarps) prefill_combine_kernel(const PfParams p) {
+    __shared__ int64_t s_end;
+    __shared__ int s_b, s_g, s_i, s_go;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x + 1;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (warp == 0) {
+        const int64_t total = pf_total(p, false);
+        const int64_t k = (total + p.num_splits - 1) / p.num_splits;
+        const int64_t at = c * k;
+        int go = 0;
+        if (k > 0 && at < total) {
+            const PfPlace w = pf_find(p, at);
+            go = w.t > 0 && w.block_start >= at - k;
+            if (go && lane == 0) {
+                const PfSeq s = pf_seq(p, w.b);
+                const int last = min((w.i + 1) * p.block_tokens, s.n);
+                s_end = (w.block_start + (s.L - s.n + last + kPfTile - 1) / kPfTile - 1) / k;  // chunk of its last pair
+                s_b = w.b; s_g = w.g; s_i = w.i;
+            }
+        }
+        if (lane == 0) s_go = go;
+    }
+    __syncthreads();
+    if (!s_go) return;
+    const PfSeq s = pf_seq(p, s_b);
+    const int first = s_i * p.block_tokens;
+    const int parts = (int)(s_end - (c - 1)) + 1;
+    for (int r = blockIdx.y * kPcRows + warp; r < (int)(blockIdx.y + 1) * kPcRows; r += kPcWarps) {
+        const int in_tile = r % kPfRows;
+        const int tok = r / kPfRows * p.tile_tokens + in_tile / p.G;
+        if (in_tile >= p.tile_tokens * p.G || first + tok >= s.n) continue;
+        // piece x of the block: slot 2 (c - 1) + 1 for the first, 2 (c - 1 + x) after it
+        auto slot = [&](int x) -> int64_t {
+            return (int64_t)(2 * (c - 1 + x) + (x == 0 ? 1 : 0)) * kPfBlockRows + r;
+        };
+        float M = -INFINITY;
+        for (int x = lane; x < parts; x += 32) M = fmaxf(M, p.lse_part[slot(x)]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.0f;
+#pragma unroll 4
+        for (int x = 0; x < parts; ++x) {
+            const int64_t sl = slot(x);
+            const float lx = p.lse_part[sl];
+            const float w = lx == -INFINITY ? 0.0f : expf(lx - M);
+            const float4 v = *reinterpret_cast<const float4 *>(p.o_part + sl * kDv + 4 * lane);
+            den += w;
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
+        const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+        const int64_t orow = (s.q0 + first + tok) * p.heads + s_g * p.G + in_tile % p.G;
+        *reinterpret_cast<uint2 *>(p.out + orow * kDv + 4 * lane) =
+            pack_bf16x4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (lane == 0 && p.lse_out) p.lse_out[orow] = den > 0.0f ? M + logf(den) : -INFINITY;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_starts, int heads, int num_groups,
+                               const void *kv, const void *k_rope, int64_t num_slots, const gqla_kv_index *idx,
+                               int num_splits, float scale, float *o_part, float *lse_part, void *out,
+                               float *lse_out, void *ws, cudaStream_t stream) {
+    const int G = heads / num_groups;
+    PfParams p;
+    p.q_starts = q_starts;
+    p.page_table = idx->page_table;
+    p.seqlens = idx->seqlens;
+    p.o_part = o_part;
+    p.lse_part = lse_part;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.lse_out = lse_out;
+    p.ws = ws;
+    p.total_q = total_q;
+    p.num_slots = num_slots;
+    p.batch = idx->batch;
+    p.max_pages = idx->max_pages_per_seq;
+    p.num_pages = idx->num_pages;
+    p.num_splits = num_splits;
+    p.heads = heads;
+    p.groups = num_groups;
+    p.G = G;
+    p.tile_tokens = pf_tile_tokens(G);
+    p.block_tokens = pf_block_tokens(G);
+    p.scale_log2 = scale * kLog2e;
+    CUtensorMap kvm, krm, qm;
+    {
+        const uint64_t dims[3] = {(uint64_t)kKv, (uint64_t)num_slots, (uint64_t)num_groups};
+        const uint64_t strides[2] = {(uint64_t)kKv * 2, (uint64_t)num_slots * kKv * 2};
+        const uint32_t box[3] = {64, 64, 1};
+        if (!make_bf16_map(&kvm, kv, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+    }
+    {
+        const uint64_t dims[2] = {(uint64_t)kRope, (uint64_t)num_slots};
+        const uint64_t strides[1] = {(uint64_t)kRope * 2};
+        const uint32_t box[2] = {64, 64};
+        if (!make_bf16_map(&krm, k_rope, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+    }
+    {  // a box is the G heads of one group for the tokens of one MMA tile
+        const uint64_t dims[3] = {(uint64_t)kQk, (uint64_t)heads, (uint64_t)total_q};
+        const uint64_t strides[2] = {(uint64_t)kQk * 2, (uint64_t)heads * kQk * 2};
+        const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)p.tile_tokens};
+        if (!make_bf16_map(&qm, q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+    }
+    cudaError_t e = cudaFuncSetAttribute(prefill_gqa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         PfSmem::kAlloc);
+    if (e != cudaSuccess) return e;
+    // the register split must not ask for more than the launch gives
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, prefill_gqa_kernel);
+    if (e != cudaSuccess) return e;
+    if (128 * kPfIssueRegs + 256 * kPfSoftmaxRegs > kPfThreads * fa.numRegs) return cudaErrorInvalidConfiguration;
+    e = launch_dependent(prefill_gqa_kernel, dim3(num_splits), dim3(kPfThreads), PfSmem::kAlloc, stream, kvm, krm, qm, p);
+    if (e != cudaSuccess || num_splits == 1) return e;
+    return launch_dependent(prefill_combine_kernel, dim3(num_splits - 1, kPfBlockRows / kPcRows),
+                            dim3(32 * kPcWarps), 0, stream, p);
+}
+
+}  // namespace gqla

@@ -26,6 +26,7 @@ _lib = ctypes.CDLL(_LIB_PATH)
 D_LATENT, D_ROPE, D_NOPE, D_V = 512, 64, 128, 128
 D_QK, D_ROW = D_NOPE + D_ROPE, D_LATENT + D_ROPE
 PAGE_SIZE = 64
+PREFILL_BLOCK_ROWS = 256  # query rows of a partial of gqla_prefill_gqa
 
 STATUS = {0: "GQLA_OK", -1: "GQLA_ERR_INVALID_ARG", -2: "GQLA_ERR_UNSUPPORTED",
           -3: "GQLA_ERR_WORKSPACE", -4: "GQLA_ERR_CUDA", -5: "GQLA_ERR_DEVICE",
@@ -70,6 +71,9 @@ _SIGS = {
     "gqla_sparse_select": [_DP, _KP, _I, _P, _I, _P, _P, _P, _P, _SZ, _P],
     "gqla_decode_gqa_sparse": [_DP, _P, _I, _P, _P, _I64, _KP, _P, _I, _P, _P, _P, _SZ, _P],
     "gqla_decode_gqa_noalloc": [_DP, _P, _I, _P, _P, _I64, _KP, _I, _P, _P, _P, _P],
+    "gqla_prefill_gqa": [_DP, _P, _I64, _P, _P, _P, _I64, _KP, _I, _P, _P, _P, _P, _P, _SZ, _P],
+    "gqla_prefill_slots": [_I],
+    "gqla_plan_prefill": [_DP, _P, _P, _I, _I],
     "gqla_partial_slots": [_I, _I],
     "gqla_workspace_bytes": [],
     "gqla_num_splits_hint": [_I, _I, _I],
@@ -293,7 +297,52 @@ def gqla_decode_gqa_noalloc(dims, q, kv_expanded, k_rope, kv, num_splits, out, l
         _stream(stream)))
 
 
+# ------------------------------------------------------------------ ragged batches of new tokens
+
+def gqla_prefill_gqa(dims, q, q_starts, kv_expanded, k_rope, kv, num_splits, o_part, lse_part, out, lse_out,
+                     workspace, stream=None):
+    """Attention of chunks of new tokens; o_part / lse_part may be None for one split."""
+    n = kv.num_pages * kv.page_size
+    h, total = dims.num_heads, q.shape[0]
+    slots = gqla_prefill_slots(num_splits)
+    _check("gqla_prefill_gqa", _lib.gqla_prefill_gqa(
+        ctypes.byref(dims), _dev(q, "q", torch.bfloat16, (total, h, D_QK)), total,
+        _dev(q_starts, "q_starts", torch.int32, (kv.batch + 1,)),
+        _dev(kv_expanded, "kv_expanded", torch.bfloat16, (dims.num_groups, n, D_NOPE + D_V)),
+        _dev(k_rope, "k_rope", torch.bfloat16, (n, D_ROPE)), n, ctypes.byref(kv), num_splits,
+        None if o_part is None else _dev(o_part, "o_part", torch.float32, (slots, PREFILL_BLOCK_ROWS, D_V)),
+        None if lse_part is None else _dev(lse_part, "lse_part", torch.float32, (slots, PREFILL_BLOCK_ROWS)),
+        _dev(out, "out", torch.bfloat16, (total, h, D_V)),
+        None if lse_out is None else _dev(lse_out, "lse_out", torch.float32, (total, h)),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
 # ------------------------------------------------------------------ helpers
+
+def gqla_prefill_slots(num_splits: int) -> int:
+    n = _lib.gqla_prefill_slots(num_splits)
+    if n < 0:
+        raise GqlaError("gqla_prefill_slots", n)
+    return n
+
+
+def gqla_plan_prefill(dims, new_tokens, seqlens, max_splits: int) -> int:
+    """Split count of gqla_prefill_gqa for known lengths (host int32 values: CPU tensors or lists)."""
+    new = torch.as_tensor(new_tokens, dtype=torch.int32, device="cpu").contiguous()
+    lens = torch.as_tensor(seqlens, dtype=torch.int32, device="cpu").contiguous()
+    if new.shape != lens.shape or new.dim() != 1:
+        raise ValueError("new_tokens and seqlens must be [batch]")
+    n = _lib.gqla_plan_prefill(ctypes.byref(dims), ctypes.c_void_p(new.data_ptr()), ctypes.c_void_p(lens.data_ptr()),
+                               lens.numel(), max_splits)
+    if n < 0:
+        raise GqlaError("gqla_plan_prefill", n)
+    return n
+
+
+def plan_prefill(dims, new_tokens, seqlens) -> int:
+    """gqla_plan_prefill up to one CTA for each SM of the current device."""
+    return gqla_plan_prefill(dims, new_tokens, seqlens, gqla_num_splits_hint("gqa", dims.num_heads, 1))
+
 
 def gqla_partial_slots(batch: int, num_splits: int) -> int:
     n = _lib.gqla_partial_slots(batch, num_splits)
@@ -415,6 +464,33 @@ class DecodeBuffers:
         self.out = torch.empty(batch, s_q, h, D_V, dtype=torch.bfloat16, device=device)
         self.lse = torch.empty(batch, s_q, h, dtype=torch.float32, device=device)
         self.workspace = new_workspace(device)
+
+
+class PrefillBuffers:
+    """Device buffers of gqla_prefill_gqa for up to total_q new tokens at one split count."""
+
+    def __init__(self, dims, total_q: int, num_splits: int, device="cuda"):
+        h, slots = dims.num_heads, gqla_prefill_slots(num_splits)
+        self.num_splits = num_splits
+        self.o_part = self.lse_part = None
+        if num_splits > 1:
+            self.o_part = torch.empty(slots, PREFILL_BLOCK_ROWS, D_V, dtype=torch.float32, device=device)
+            self.lse_part = torch.empty(slots, PREFILL_BLOCK_ROWS, dtype=torch.float32, device=device)
+        self.out = torch.empty(total_q, h, D_V, dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty(total_q, h, dtype=torch.float32, device=device)
+        self.workspace = new_workspace(device)
+
+
+def prefill_step(dims, bufs: PrefillBuffers, q, q_starts, kv, kv_expanded, k_rope, stream=None):
+    """Attention of the new tokens q [total_q][h][192] through the C ABI.  Returns
+    (out [total_q][h][128] bf16, lse [total_q][h])."""
+    total = q.shape[0]
+    if total > bufs.out.shape[0]:
+        raise ValueError(f"q has {total} tokens, the buffers hold {bufs.out.shape[0]}")
+    out, lse = bufs.out[:total], bufs.lse[:total]
+    gqla_prefill_gqa(dims, q, q_starts, kv_expanded, k_rope, kv, bufs.num_splits, bufs.o_part, bufs.lse_part,
+                     out, lse, bufs.workspace, stream)
+    return out, lse
 
 
 class SparseBuffers:

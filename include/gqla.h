@@ -302,6 +302,48 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
                       gqla_stream_t stream);
 
 /*
+ * Attention of chunks of new tokens (prefill, chunked prefill, verification of
+ * draft tokens), GQA path: sequence b brings n_b = q_starts[b + 1] - q_starts[b]
+ * new tokens, which are already the last n_b of its L_b cached tokens, and query
+ * i of sequence b sees tokens t <= L_b - n_b + i.  The batch is ragged: any mix of
+ * lengths from 0 and 1 up, with or without tokens cached before.
+ *   q            bf16 [total_q][h][192]; rows q_starts[b] + i
+ *   q_starts     device int32 [batch + 1], 0 <= q_starts[b] <= q_starts[b + 1] <= total_q
+ *   kv_expanded, k_rope, num_slots, kv   the expanded cache, as for gqla_decode_gqa;
+ *                kv->seqlens counts the new tokens
+ *   num_splits   C >= 1: the batch's (query block, group, key tile) triples are cut
+ *                into C equal chunks, one per CTA (gqla_plan_prefill picks C)
+ *   o_part       fp32 [gqla_prefill_slots(C)][256][128], lse_part fp32
+ *                [gqla_prefill_slots(C)][256]: partials of the query blocks that a cut
+ *                divides; may be NULL when C == 1
+ *   out          bf16 [total_q][h][128];  lse_out fp32 [total_q][h] or NULL (natural
+ *                log, as from gqla_combine).  Rows that belong to no sequence are left
+ *                as they were.
+ * Any number of groups, 1 <= h/g <= 128 (GQLA_ERR_UNSUPPORTED otherwise).  A
+ * sequence whose numbers are inconsistent (descending or out-of-range q_starts,
+ * n_b > L_b, L_b beyond its page-table row) is reported (GQLA_ERR_DEVICE, info = b)
+ * and its rows are left as they were; a page index outside the pool is reported the
+ * same way and leaves that sequence's rows unspecified.  Cached rows past L_b may hold
+ * anything, NaN too.
+ * Precision: bf16 operands, scores, softmax and its sum in fp32, P rounded to bf16
+ * (the tensor-core operand), O accumulated in fp32, one rounding to bf16.
+ */
+int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, const int32_t *q_starts,
+                     const void *kv_expanded, const void *k_rope, int64_t num_slots, const gqla_kv_index *kv,
+                     int num_splits, float *o_part, float *lse_part, void *out, float *lse_out,
+                     void *workspace, size_t workspace_bytes, gqla_stream_t stream);
+
+/* Partial slots (256 rows each) that gqla_prefill_gqa addresses: 2 * num_splits. */
+int gqla_prefill_slots(int num_splits);
+
+/* Host-side choice of gqla_prefill_gqa's num_splits for known lengths.
+ *   new_tokens, seqlens   host int32 [batch], 0 <= new_tokens[b] <= seqlens[b]
+ *   max_splits            1 .. 65535 (the SM count: gqla_num_splits_hint(1, ...))
+ * Returns the split count, or GQLA_ERR_INVALID_ARG / GQLA_ERR_UNSUPPORTED. */
+int gqla_plan_prefill(const gqla_dims *dims, const int32_t *new_tokens, const int32_t *seqlens, int batch,
+                      int max_splits);
+
+/*
  * GQA-path decode step that allocates nothing: gqla_decode_gqa followed by
  * gqla_combine, with the split partials, their LSEs and the device error
  * record kept in a file-scope device array owned by the library.  The pages
