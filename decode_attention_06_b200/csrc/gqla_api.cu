@@ -41,6 +41,18 @@ cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_
                                const void *kv, const void *k_rope, int64_t num_slots, const gqla_kv_index *idx,
                                int num_splits, float scale, float *o_part, float *lse_part, void *out,
                                float *lse_out, void *ws, cudaStream_t stream);
+cudaError_t launch_append(const void *rows, int64_t total, const int32_t *q_starts, const void *w_uk,
+                          const void *w_uv, int num_groups, void *latent, void *kv, void *k_rope, int64_t num_slots,
+                          const gqla_kv_index *idx, void *ws, cudaStream_t stream);
+int64_t copy_pages_limit();
+cudaError_t launch_copy_pages(const int32_t *pairs, int64_t n, int num_pages, int num_groups, void *latent, void *kv,
+                              void *k_rope, void *ws, cudaStream_t stream);
+cudaError_t launch_fork(const gqla_page_pool *pool, const int32_t *forks, int n, int32_t *pairs, void *ws,
+                        cudaStream_t stream);
+cudaError_t launch_extend(const gqla_page_pool *pool, const int32_t *new_tokens, void *ws, cudaStream_t stream);
+cudaError_t launch_free(const gqla_page_pool *pool, const int32_t *ids, int n, void *ws, cudaStream_t stream);
+cudaError_t launch_compact(const gqla_page_pool *pool, int32_t *table_out, int32_t *refs_out, int32_t *pairs,
+                           int32_t *counts, void *ws, cudaStream_t stream);
 int group_splits_rule(int num_splits, int num_groups, int sms);
 extern thread_local int g_drop_v_unit;
 }  // namespace gqla
@@ -51,6 +63,7 @@ namespace {
 
 constexpr size_t kWorkspaceBytes = 256;
 
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // A lead of 0 .. num_splits chunks, each 1 to 64 times as long as the others (in 1/16).
@@ -87,6 +100,13 @@ int check_ragged_dims(const gqla_dims *d) {
     if (!(d->softmax_scale > 0.0f) || !isfinite(d->softmax_scale)) return GQLA_ERR_INVALID_ARG;
     if (!dims_supported(d)) return GQLA_ERR_UNSUPPORTED;
     if (d->num_heads / d->num_groups > kPfRows) return GQLA_ERR_UNSUPPORTED;
+    return GQLA_OK;
+}
+
+int check_pool(const gqla_page_pool *p) {
+    if (!p || !p->page_table || !p->seqlens || !p->page_refs) return GQLA_ERR_INVALID_ARG;
+    if (p->batch <= 0 || p->max_pages_per_seq <= 0 || p->num_pages <= 0) return GQLA_ERR_INVALID_ARG;
+    if (p->batch > 65535 || p->page_size != kPage) return GQLA_ERR_UNSUPPORTED;
     return GQLA_OK;
 }
 
@@ -498,6 +518,85 @@ int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, cons
     return cuda_status(launch_prefill_gqa(q, total_q, q_starts, dims->num_heads, dims->num_groups, kv_expanded,
                                           k_rope, num_slots, kv, num_splits, dims->softmax_scale, o_part, lse_part,
                                           out, lse_out, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gqla_append_cache(const gqla_dims *dims, const void *rows, int64_t total_q, const int32_t *q_starts,
+                      const void *w_uk, const void *w_uv, void *latent_cache, void *kv_expanded, void *k_rope,
+                      int64_t num_slots, const gqla_kv_index *kv, void *workspace, size_t workspace_bytes,
+                      gqla_stream_t stream) {
+    int st = check_ragged_dims(dims);
+    if (st != GQLA_OK) return st;
+    if ((st = check_index(kv)) != GQLA_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
+    if (total_q < 0 || !rows || !q_starts) return GQLA_ERR_INVALID_ARG;
+    // the expanded cache has two parts and takes both weights; at least one cache is written
+    if ((kv_expanded == nullptr) != (k_rope == nullptr)) return GQLA_ERR_INVALID_ARG;
+    if (kv_expanded ? (!w_uk || !w_uv) : !latent_cache) return GQLA_ERR_INVALID_ARG;
+    if (!aligned16(rows) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(latent_cache) ||
+        !aligned16(kv_expanded) || !aligned16(k_rope))
+        return GQLA_ERR_INVALID_ARG;
+    if (num_slots != (int64_t)kv->num_pages * kv->page_size) return GQLA_ERR_INVALID_ARG;
+    const int64_t most = ((int64_t)1 << 31) - 1;
+    if (total_q > most || num_slots > most || dims->num_groups > 4096) return GQLA_ERR_UNSUPPORTED;
+    if (total_q == 0) return GQLA_OK;
+    return cuda_status(launch_append(rows, total_q, q_starts, w_uk, w_uv, dims->num_groups, latent_cache, kv_expanded,
+                                     k_rope, num_slots, kv, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gqla_copy_pages(const gqla_dims *dims, const int32_t *pairs, int64_t num_pairs, int num_pages, void *latent_cache,
+                    void *kv_expanded, void *k_rope, void *workspace, size_t workspace_bytes, gqla_stream_t stream) {
+    int st = check_ragged_dims(dims);
+    if (st != GQLA_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
+    if (num_pairs < 0 || num_pages <= 0 || !pairs || !aligned8(pairs)) return GQLA_ERR_INVALID_ARG;
+    if (!latent_cache && !kv_expanded && !k_rope) return GQLA_ERR_INVALID_ARG;
+    if (!aligned16(latent_cache) || !aligned16(kv_expanded) || !aligned16(k_rope)) return GQLA_ERR_INVALID_ARG;
+    if (num_pages > copy_pages_limit() || num_pairs > ((int64_t)1 << 31) - 1 || dims->num_groups > 4096)
+        return GQLA_ERR_UNSUPPORTED;
+    if (num_pairs == 0) return GQLA_OK;
+    return cuda_status(launch_copy_pages(pairs, num_pairs, num_pages, dims->num_groups, latent_cache, kv_expanded,
+                                         k_rope, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gqla_fork_sequences(const gqla_page_pool *pool, const int32_t *forks, int num_forks, int32_t *pairs,
+                        void *workspace, size_t workspace_bytes, gqla_stream_t stream) {
+    int st = check_pool(pool);
+    if (st != GQLA_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
+    if (num_forks < 0 || !forks || !pairs || !aligned8(forks) || !aligned8(pairs)) return GQLA_ERR_INVALID_ARG;
+    if (num_forks > 65535) return GQLA_ERR_UNSUPPORTED;
+    if (num_forks == 0) return GQLA_OK;
+    return cuda_status(launch_fork(pool, forks, num_forks, pairs, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gqla_extend_sequences(const gqla_page_pool *pool, const int32_t *new_tokens, void *workspace,
+                          size_t workspace_bytes, gqla_stream_t stream) {
+    int st = check_pool(pool);
+    if (st != GQLA_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
+    if (!new_tokens) return GQLA_ERR_INVALID_ARG;
+    return cuda_status(launch_extend(pool, new_tokens, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gqla_free_sequences(const gqla_page_pool *pool, const int32_t *seq_ids, int num_ids, void *workspace,
+                        size_t workspace_bytes, gqla_stream_t stream) {
+    int st = check_pool(pool);
+    if (st != GQLA_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
+    if (num_ids < 0 || !seq_ids) return GQLA_ERR_INVALID_ARG;
+    if (num_ids > 65535) return GQLA_ERR_UNSUPPORTED;
+    if (num_ids == 0) return GQLA_OK;
+    return cuda_status(launch_free(pool, seq_ids, num_ids, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gqla_compact_pages(const gqla_page_pool *pool, int32_t *page_table_out, int32_t *page_refs_out, int32_t *pairs,
+                       int32_t *counts, void *workspace, size_t workspace_bytes, gqla_stream_t stream) {
+    int st = check_pool(pool);
+    if (st != GQLA_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
+    if (!page_table_out || !page_refs_out || !pairs || !counts || !aligned8(pairs)) return GQLA_ERR_INVALID_ARG;
+    return cuda_status(launch_compact(pool, page_table_out, page_refs_out, pairs, counts, workspace,
+                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

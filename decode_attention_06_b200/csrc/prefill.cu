@@ -30,6 +30,7 @@
 
 #include "common.cuh"
 #include "prefill_plan.cuh"
+#include "ragged.cuh"
 #include "sm100.cuh"
 #include "tensor_map.cuh"
 
@@ -91,23 +92,10 @@ __device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity, v
     }
 }
 
-// New tokens n, cached tokens L and first query row of a sequence; n = 0 for a sequence
-// without new tokens and for one whose numbers are inconsistent (reported by `bad`).
-struct PfSeq {
-    int n, L;
-    int64_t q0;
-    bool bad;
-};
+using PfSeq = RaggedSeq;
 
 __device__ __forceinline__ PfSeq pf_seq(const PfParams &p, int b) {
-    const int a = p.q_starts[b], e = p.q_starts[b + 1], L = p.seqlens[b];
-    PfSeq s;
-    s.bad = a < 0 || e < a || (int64_t)e > p.total_q || (e > a && L < e - a) ||
-            (int64_t)L > (int64_t)p.max_pages * kPage;
-    s.n = s.bad ? 0 : e - a;
-    s.L = L;
-    s.q0 = a;
-    return s;
+    return ragged_seq(p.q_starts, p.seqlens, b, p.total_q, p.max_pages);
 }
 
 __device__ __forceinline__ int64_t pf_seq_tiles(const PfParams &p, const PfSeq &s) {

@@ -55,8 +55,16 @@ class gqla_kv_index(ctypes.Structure):
                 ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int)]
 
 
+class gqla_page_pool(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("seqlens", ctypes.c_void_p),
+                ("page_refs", ctypes.c_void_p), ("batch", ctypes.c_int),
+                ("max_pages_per_seq", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int)]
+
+
 _P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 _DP, _KP = ctypes.POINTER(gqla_dims), ctypes.POINTER(gqla_kv_index)
+_PP = ctypes.POINTER(gqla_page_pool)
 _SIGS = {
     "gqla_expand_cache": [_DP, _P, _I64, _P, _P, _P, _P, _P],
     "gqla_expand_cache_tc": [_DP, _P, _I64, _P, _P, _P, _P, _P],
@@ -74,6 +82,12 @@ _SIGS = {
     "gqla_prefill_gqa": [_DP, _P, _I64, _P, _P, _P, _I64, _KP, _I, _P, _P, _P, _P, _P, _SZ, _P],
     "gqla_prefill_slots": [_I],
     "gqla_plan_prefill": [_DP, _P, _P, _I, _I],
+    "gqla_append_cache": [_DP, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _KP, _P, _SZ, _P],
+    "gqla_copy_pages": [_DP, _P, _I64, _I, _P, _P, _P, _P, _SZ, _P],
+    "gqla_fork_sequences": [_PP, _P, _I, _P, _P, _SZ, _P],
+    "gqla_extend_sequences": [_PP, _P, _P, _SZ, _P],
+    "gqla_free_sequences": [_PP, _P, _I, _P, _SZ, _P],
+    "gqla_compact_pages": [_PP, _P, _P, _P, _P, _P, _SZ, _P],
     "gqla_partial_slots": [_I, _I],
     "gqla_workspace_bytes": [],
     "gqla_num_splits_hint": [_I, _I, _I],
@@ -134,6 +148,18 @@ def make_kv_index(page_table: torch.Tensor, seqlens: torch.Tensor, num_pages: in
     idx = gqla_kv_index(pt, sl, page_table.shape[0], page_table.shape[1], page_size, num_pages)
     idx._keep = (page_table, seqlens)  # keep the tensors alive with the struct
     return idx
+
+
+def make_page_pool(page_table: torch.Tensor, seqlens: torch.Tensor, page_refs: torch.Tensor,
+                   page_size: int = PAGE_SIZE):
+    """The tables that the page calls write; page_refs[p] = used table entries that name p."""
+    pt, sl = _dev(page_table, "page_table", torch.int32), _dev(seqlens, "seqlens", torch.int32)
+    rf = _dev(page_refs, "page_refs", torch.int32)
+    if page_table.dim() != 2 or seqlens.shape != (page_table.shape[0],) or page_refs.dim() != 1:
+        raise ValueError("page_table must be [batch][max_pages], seqlens [batch] and page_refs [num_pages]")
+    pool = gqla_page_pool(pt, sl, rf, page_table.shape[0], page_table.shape[1], page_size, page_refs.shape[0])
+    pool._keep = (page_table, seqlens, page_refs)
+    return pool
 
 
 # ------------------------------------------------------------------ the five calls
@@ -314,6 +340,76 @@ def gqla_prefill_gqa(dims, q, q_starts, kv_expanded, k_rope, kv, num_splits, o_p
         None if lse_part is None else _dev(lse_part, "lse_part", torch.float32, (slots, PREFILL_BLOCK_ROWS)),
         _dev(out, "out", torch.bfloat16, (total, h, D_V)),
         None if lse_out is None else _dev(lse_out, "lse_out", torch.float32, (total, h)),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def gqla_append_cache(dims, rows, q_starts, kv, workspace, latent_cache=None, w_uk=None, w_uv=None,
+                      kv_expanded=None, k_rope=None, stream=None):
+    """The latent rows of new tokens into the caches that are given (latent, expanded + RoPE keys)."""
+    n, total, g = kv.num_pages * kv.page_size, rows.shape[0], dims.num_groups
+    _check("gqla_append_cache", _lib.gqla_append_cache(
+        ctypes.byref(dims), _dev(rows, "rows", torch.bfloat16, (total, D_ROW)), total,
+        _dev(q_starts, "q_starts", torch.int32, (kv.batch + 1,)),
+        None if w_uk is None else _dev(w_uk, "w_uk", torch.bfloat16, (g, D_LATENT, D_NOPE)),
+        None if w_uv is None else _dev(w_uv, "w_uv", torch.bfloat16, (g, D_LATENT, D_V)),
+        *_caches(dims, kv.num_pages, latent_cache, kv_expanded, k_rope), n, ctypes.byref(kv),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ------------------------------------------------------------------ the pages of a cache
+
+def _caches(dims, num_pages, latent_cache, kv_expanded, k_rope):
+    n = num_pages * PAGE_SIZE
+    return (None if latent_cache is None else
+            _dev(latent_cache, "latent_cache", torch.bfloat16, (num_pages, PAGE_SIZE, D_ROW)),
+            None if kv_expanded is None else
+            _dev(kv_expanded, "kv_expanded", torch.bfloat16, (dims.num_groups, n, D_NOPE + D_V)),
+            None if k_rope is None else _dev(k_rope, "k_rope", torch.bfloat16, (n, D_ROPE)))
+
+
+def _pairs(t, name, rows=None):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] != 2 or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'n' if rows is None else rows}][2]")
+    return _dev(t, name, torch.int32)
+
+
+def gqla_copy_pages(dims, pairs, num_pages, workspace, latent_cache=None, kv_expanded=None, k_rope=None, stream=None):
+    """Pages pairs[i] = (source, target) of the given caches; a negative source is skipped."""
+    _check("gqla_copy_pages", _lib.gqla_copy_pages(
+        ctypes.byref(dims), _pairs(pairs, "pairs"), pairs.shape[0], num_pages,
+        *_caches(dims, num_pages, latent_cache, kv_expanded, k_rope),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def gqla_fork_sequences(pool, forks, pairs, workspace, stream=None):
+    """forks[i] = (parent, child); pairs[i] receives the page copy that the fork needs, or (-1, -1)."""
+    _check("gqla_fork_sequences", _lib.gqla_fork_sequences(
+        ctypes.byref(pool), _pairs(forks, "forks"), forks.shape[0], _pairs(pairs, "pairs", forks.shape[0]),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def gqla_extend_sequences(pool, new_tokens, workspace, stream=None):
+    """new_tokens[b] more tokens (and the pages for them) for every sequence."""
+    _check("gqla_extend_sequences", _lib.gqla_extend_sequences(
+        ctypes.byref(pool), _dev(new_tokens, "new_tokens", torch.int32, (pool.batch,)),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def gqla_free_sequences(pool, seq_ids, workspace, stream=None):
+    if seq_ids.dim() != 1:
+        raise ValueError("seq_ids must be [n]")
+    _check("gqla_free_sequences", _lib.gqla_free_sequences(
+        ctypes.byref(pool), _dev(seq_ids, "seq_ids", torch.int32), seq_ids.shape[0],
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def gqla_compact_pages(pool, page_table_out, page_refs_out, pairs, counts, workspace, stream=None):
+    """Live pages to the front; pairs receives the moves (gqla_copy_pages), counts = (live pages, moves).
+    The outputs may be the pool's own tables."""
+    _check("gqla_compact_pages", _lib.gqla_compact_pages(
+        ctypes.byref(pool), _dev(page_table_out, "page_table_out", torch.int32, (pool.batch, pool.max_pages_per_seq)),
+        _dev(page_refs_out, "page_refs_out", torch.int32, (pool.num_pages,)),
+        _pairs(pairs, "pairs", max(1, pool.num_pages // 2)), _dev(counts, "counts", torch.int32, (2,)),
         _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 

@@ -344,6 +344,107 @@ int gqla_plan_prefill(const gqla_dims *dims, const int32_t *new_tokens, const in
                       int max_splits);
 
 /*
+ * Append: the latent rows of new tokens into the pages of the caches, and for the
+ * GQA path their per-group expansion, in one call (what gqla_expand_cache_tc does to a
+ * whole cache, done to the tokens of one step, chunk or prompt; before gqla_prefill_gqa
+ * or a decode of the same step).  Row q_starts[b] + i is the token at position
+ * L_b - n_b + i of sequence b.
+ *   rows          bf16 [total_q][576]: [c | k^R]
+ *   q_starts, kv  as for gqla_prefill_gqa: kv->seqlens counts the new tokens, whose
+ *                 pages are already in the table (gqla_extend_sequences)
+ *   latent_cache  bf16 [num_slots][576] or NULL
+ *   kv_expanded, k_rope   as for gqla_expand_cache, or both NULL (then the weights
+ *                 may be NULL too); at least one of the two caches is given
+ * Accumulation and accuracy as for gqla_expand_cache_tc; latent rows and RoPE keys are
+ * copied exactly.  Sequences with inconsistent numbers are reported and left out as by
+ * gqla_prefill_gqa, and so are tokens whose page is outside the pool.  Two sequences
+ * of the batch must not share the page of a new token (gqla_fork_sequences gives a
+ * fork a page of its own for that).
+ */
+int gqla_append_cache(const gqla_dims *dims, const void *rows, int64_t total_q, const int32_t *q_starts,
+                      const void *w_uk, const void *w_uv, void *latent_cache, void *kv_expanded, void *k_rope,
+                      int64_t num_slots, const gqla_kv_index *kv, void *workspace, size_t workspace_bytes,
+                      gqla_stream_t stream);
+
+/*
+ * The pages of a cache, managed on the device.  A pool is a page table and lengths
+ * (those of gqla_kv_index, written here) and page_refs: how many used page-table
+ * entries (the first ceil(L_b / 64) of each row) name each page; 0 is a free page.
+ * Page indices are the same for every cache laid out over the pool (latent, expanded,
+ * RoPE keys, of one layer or many): the table calls run once per step, the copies once
+ * per layer.  New pages are the lowest free ones, in list order, so results do not
+ * depend on timing.  Each call's first device-side error goes to its workspace; what is
+ * in error is left out, the rest is done.
+ */
+typedef struct {
+    int32_t *page_table;   /* device int32 [batch][max_pages_per_seq] */
+    int32_t *seqlens;      /* device int32 [batch]                    */
+    int32_t *page_refs;    /* device int32 [num_pages]                */
+    int batch;             /* 1..65535                                */
+    int max_pages_per_seq;
+    int page_size;         /* 64                                      */
+    int num_pages;
+} gqla_page_pool;
+
+/*
+ * Copies whole pages within each given cache (latent_cache bf16 [num_pages][64][576],
+ * kv_expanded bf16 [g][num_pages * 64][256], k_rope bf16 [num_pages * 64][64]; NULL
+ * leaves one out).
+ *   pairs   device int32 [num_pairs][2], 8-byte aligned: {source, target}; a negative
+ *           source or a page onto itself is skipped
+ * A pair with a page outside the pool, one whose target another pair writes too, and
+ * one whose source another pair writes are reported (GQLA_ERR_DEVICE, info = pair) and
+ * left out.  num_pages <= 524288 (GQLA_ERR_UNSUPPORTED beyond).
+ */
+int gqla_copy_pages(const gqla_dims *dims, const int32_t *pairs, int64_t num_pairs, int num_pages, void *latent_cache,
+                    void *kv_expanded, void *k_rope, void *workspace, size_t workspace_bytes, gqla_stream_t stream);
+
+/*
+ * Forks sequences: the child gets the parent's length and full pages (their counts
+ * rise by one) and, for a last page that is partly filled, a fresh page, so that both
+ * can go on appending.  pairs[i] = {parent's last page, fresh page}, or {-1, -1}: pass
+ * them to gqla_copy_pages for each cache.
+ *   forks   device int32 [num_forks][2], 8-byte aligned: {parent, child}; children are
+ *           empty (length 0), named once, and no parents of the same call; a parent may
+ *           be named any number of times.  num_forks <= 65535
+ *   pairs   device int32 [num_forks][2], out
+ * A fork that breaks these rules, or finds no free page, is reported (info = its index)
+ * and its child stays empty.
+ */
+int gqla_fork_sequences(const gqla_page_pool *pool, const int32_t *forks, int num_forks, int32_t *pairs,
+                        void *workspace, size_t workspace_bytes, gqla_stream_t stream);
+
+/*
+ * Extends every sequence by new_tokens[b] >= 0 tokens (device int32 [batch]): its pages
+ * from the free ones, sequence after sequence, then its length.  A sequence whose pages
+ * do not all fit (or whose row is too short, or a negative number) is reported
+ * (info = b) and unchanged, and once the free pages have run out so is every later one
+ * that needs a page.
+ */
+int gqla_extend_sequences(const gqla_page_pool *pool, const int32_t *new_tokens, void *workspace,
+                          size_t workspace_bytes, gqla_stream_t stream);
+
+/*
+ * Frees sequences (device int32 [num_ids], num_ids <= 65535): the counts of their pages
+ * fall by one, their lengths become 0; table rows are left as they are.  A sequence
+ * named twice is freed once.
+ */
+int gqla_free_sequences(const gqla_page_pool *pool, const int32_t *seq_ids, int num_ids, void *workspace,
+                        size_t workspace_bytes, gqla_stream_t stream);
+
+/*
+ * Compacts the pool: with N live pages, the live pages of index >= N move to the free
+ * ones below N, ascending to ascending, so that pages [N, num_pages) are free.
+ *   page_table_out  int32 [batch][max_pages_per_seq], page_refs_out int32 [num_pages]:
+ *           the table and the counts after the moves; may be the pool's own
+ *   pairs   device int32 [max(1, num_pages / 2)][2], out: the moves {from, to}, then
+ *           {-1, -1}; pass them to gqla_copy_pages for each cache
+ *   counts  device int32 [2], out: {N, moves}
+ */
+int gqla_compact_pages(const gqla_page_pool *pool, int32_t *page_table_out, int32_t *page_refs_out, int32_t *pairs,
+                       int32_t *counts, void *workspace, size_t workspace_bytes, gqla_stream_t stream);
+
+/*
  * GQA-path decode step that allocates nothing: gqla_decode_gqa followed by
  * gqla_combine, with the split partials, their LSEs and the device error
  * record kept in a file-scope device array owned by the library.  The pages

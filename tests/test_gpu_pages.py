@@ -1,0 +1,294 @@
+"""The page calls on the GPU against the same rules written out in Python lists: tables,
+lengths, counts, pairs and page contents are equal."""
+import random
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+class Pool:
+    """The rules of include/gqla.h, one sequence and one page at a time."""
+
+    def __init__(self, batch, width, pages):
+        self.table = [[-3] * width for _ in range(batch)]
+        self.lens, self.refs, self.width = [0] * batch, [0] * pages, width
+
+    def free_page(self):
+        return next((i for i, r in enumerate(self.refs) if r == 0), None)
+
+    def extend(self, grow):
+        bad, full = [], False
+        for b, n in enumerate(grow):
+            if n == 0:
+                continue
+            if n < 0 or self.lens[b] + n > self.width * 64:
+                bad.append(b)
+                continue
+            have, want = -(-self.lens[b] // 64), -(-(self.lens[b] + n) // 64)
+            free = [i for i, r in enumerate(self.refs) if r == 0]
+            if want > have and (full or want - have > len(free)):
+                full = True
+                bad.append(b)
+                continue
+            for j, p in zip(range(have, want), free):
+                self.table[b][j] = p
+                self.refs[p] = 1
+            self.lens[b] += n
+        return bad
+
+    def fork(self, forks):
+        kids = [c for _, c in forks]
+        lens = list(self.lens)
+        pairs, bad = [], []
+        for i, (a, c) in enumerate(forks):
+            ok = 0 <= a < len(lens) and 0 <= c < len(lens) and a != c and kids.count(c) == 1 and a not in kids and lens[c] == 0
+            page = self.free_page() if ok and lens[a] % 64 else None
+            if not ok or (lens[a] % 64 and page is None):
+                pairs.append((-1, -1))
+                bad.append(i)
+                continue
+            for j in range(lens[a] // 64):
+                self.table[c][j] = self.table[a][j]
+                self.refs[self.table[a][j]] += 1
+            pairs.append((-1, -1))
+            if lens[a] % 64:
+                pairs[-1] = (self.table[a][lens[a] // 64], page)
+                self.table[c][lens[a] // 64] = page
+                self.refs[page] = 1
+            self.lens[c] = lens[a]
+        return pairs, bad
+
+    def free(self, ids):
+        bad = []
+        for i, b in enumerate(ids):
+            if not 0 <= b < len(self.lens):
+                bad.append(i)
+                continue
+            for p in self.table[b][:-(-self.lens[b] // 64)]:
+                self.refs[p] -= 1
+            self.lens[b] = 0
+        return bad
+
+    def compact(self):
+        n = sum(r > 0 for r in self.refs)
+        moves = list(zip([i for i in range(n, len(self.refs)) if self.refs[i] > 0],
+                         [i for i in range(n) if self.refs[i] == 0]))
+        to = dict(moves)
+        for b, row in enumerate(self.table):
+            for j in range(-(-self.lens[b] // 64)):
+                row[j] = to.get(row[j], row[j])
+        for a, c in moves:
+            self.refs[c], self.refs[a] = self.refs[a], 0
+        return n, moves
+
+
+class Gpu:
+    def __init__(self, ref, groups=2, seed=0, caches=True):
+        from decode_attention_06_b200 import gqla
+        self.gqla = gqla
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+        self.i32 = i32
+        self.table, self.lens, self.refs = i32(ref.table), i32(ref.lens), i32(ref.refs)
+        self.pool = gqla.make_page_pool(self.table, self.lens, self.refs)
+        self.ws, self.dims = gqla.new_workspace(), gqla.make_dims(16 * groups, groups)
+        self.pages = len(ref.refs)
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        bf = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+        if caches:
+            self.latent, self.kv, self.rope = bf(self.pages, 64, 576), bf(groups, self.pages * 64, 256), bf(self.pages * 64, 64)
+
+    def same(self, ref):
+        assert self.lens.tolist() == ref.lens
+        assert self.refs.tolist() == ref.refs
+        assert self.table.tolist() == ref.table
+
+    def error(self, bad):
+        """The recorded error is one of the expected ones (the first to be recorded); clears it."""
+        st, info = self.gqla.gqla_read_device_error(self.ws)
+        assert (st == -5 and info in bad) if bad else st == 0, (st, info, bad)
+        self.gqla.gqla_clear_device_error(self.ws)
+
+    def extend(self, grow):
+        self.gqla.gqla_extend_sequences(self.pool, self.i32(grow), self.ws)
+
+    def fork(self, forks):
+        pairs = torch.full((len(forks), 2), 99, dtype=torch.int32).cuda()
+        self.gqla.gqla_fork_sequences(self.pool, self.i32(forks), pairs, self.ws)
+        return pairs
+
+    def free(self, ids):
+        self.gqla.gqla_free_sequences(self.pool, self.i32(ids), self.ws)
+
+    def compact(self, inplace=True):
+        t, r = (self.table, self.refs) if inplace else (torch.empty_like(self.table), torch.full_like(self.refs, 77))
+        pairs = torch.full((max(1, self.pages // 2), 2), 99, dtype=torch.int32).cuda()
+        counts = torch.zeros(2, dtype=torch.int32).cuda()
+        self.gqla.gqla_compact_pages(self.pool, t, r, pairs, counts, self.ws)
+        return t, r, pairs, counts
+
+    def copy(self, pairs, **which):
+        which = which or dict(latent_cache=self.latent, kv_expanded=self.kv, k_rope=self.rope)
+        self.gqla.gqla_copy_pages(self.dims, pairs, self.pages, self.ws, **which)
+
+
+def copied(caches, groups, pairs):
+    """The page contents after `pairs`, by indexing."""
+    latent, kv, rope = (x.clone() for x in caches)
+    kv4, rope3 = kv.view(groups, -1, 64, 256), rope.view(-1, 64, 64)
+    src = torch.tensor([a for a, _ in pairs], dtype=torch.long).cuda()
+    dst = torch.tensor([b for _, b in pairs], dtype=torch.long).cuda()
+    if len(pairs):
+        latent[dst], kv4[:, dst], rope3[dst] = latent[src], kv4[:, src], rope3[src]
+    return latent, kv, rope
+
+
+@pytest.mark.parametrize("pages,n", [(2, 1), (40, 7), (600, 250), (33, 16)])
+@pytest.mark.parametrize("groups", [1, 8])
+def test_copy_pages(pages, n, groups):
+    g = Gpu(Pool(1, 1, pages), groups)
+    order = random.Random(pages).sample(range(pages), 2 * n)
+    pairs = [(order[2 * i], order[2 * i + 1]) for i in range(n)]
+    if n > 3:
+        pairs[1] = (pairs[0][0], pairs[1][1])  # one page to two
+    want = copied((g.latent, g.kv, g.rope), groups, pairs)
+    listed = [(-1, -1), (5 % pages, 5 % pages)] + pairs + [(-1, 3 % pages)]
+    g.copy(torch.tensor(listed, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    g.error([])
+    for got, exp in zip((g.latent, g.kv, g.rope), want):
+        assert torch.equal(got, exp)
+
+
+def test_copy_pages_of_one_cache_leaves_the_others():
+    g = Gpu(Pool(1, 1, 6), 2)
+    before = [x.clone() for x in (g.latent, g.kv, g.rope)]
+    pairs = torch.tensor([[0, 4], [1, 5]], dtype=torch.int32).cuda()
+    want = copied(before, 2, [(0, 4), (1, 5)])
+    g.copy(pairs, kv_expanded=g.kv)
+    torch.cuda.synchronize()
+    assert torch.equal(g.kv, want[1]) and torch.equal(g.latent, before[0]) and torch.equal(g.rope, before[2])
+    g.copy(pairs, latent_cache=g.latent)
+    torch.cuda.synchronize()
+    assert torch.equal(g.latent, want[0]) and torch.equal(g.rope, before[2])
+    g.error([])
+
+
+def test_copy_pages_leaves_out_clashing_pairs():
+    """A target written twice, a source that another pair writes, pages outside the pool."""
+    g = Gpu(Pool(1, 1, 12), 2)
+    listed = [(0, 8), (1, 8), (2, 9), (9, 10), (3, 12), (13, 4), (5, -2), (6, 11)]
+    want = copied((g.latent, g.kv, g.rope), 2, [(2, 9), (6, 11)])
+    g.copy(torch.tensor(listed, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    g.error([0, 1, 3, 4, 5, 6])
+    for got, exp in zip((g.latent, g.kv, g.rope), want):
+        assert torch.equal(got, exp)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_lifetimes(seed):
+    """Extend, fork (with the copies), free and compact in random turns, full pools included."""
+    rng = random.Random(seed)
+    batch, width = rng.choice([(3, 4), (40, 9), (70, 30)])
+    ref = Pool(batch, width, rng.choice([7, 100, 1500]))
+    g = Gpu(ref, 2, seed)
+    for turn in range(25):
+        what = rng.choice(["extend", "fork", "free", "compact"]) if turn else "extend"
+        if what == "extend":
+            grow = [rng.choice([0, 0, 1, 5, 64, 65, rng.randint(0, 600)]) for _ in range(batch)]
+            g.extend(grow)
+            bad = ref.extend(grow)
+        elif what == "fork":
+            forks = [(rng.randrange(batch), rng.randrange(batch)) for _ in range(rng.randint(1, batch))]
+            before = (g.latent, g.kv, g.rope)
+            pairs = g.fork(forks)
+            exp, bad = ref.fork(forks)
+            assert pairs.tolist() == [list(p) for p in exp]
+            want = copied(before, 2, [p for p in exp if p[0] >= 0])
+            g.copy(pairs)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip((g.latent, g.kv, g.rope), want))
+        elif what == "free":
+            ids = [rng.randrange(batch) for _ in range(rng.randint(1, batch))]
+            g.free(ids)
+            bad = ref.free(ids)
+        else:
+            t, r, pairs, counts = g.compact(inplace=rng.random() < 0.5)
+            n, moves = ref.compact()
+            bad = []
+            torch.cuda.synchronize()
+            assert counts.tolist() == [n, len(moves)]
+            assert pairs.tolist() == [list(m) for m in moves] + [[-1, -1]] * (pairs.shape[0] - len(moves))
+            want = copied((g.latent, g.kv, g.rope), 2, moves)
+            g.copy(pairs)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip((g.latent, g.kv, g.rope), want))
+            g.table.copy_(t)
+            g.refs.copy_(r)
+        torch.cuda.synchronize()
+        g.same(ref)
+        g.error(bad)
+
+
+def test_large_batch_and_pool():
+    """More sequences than a block has threads, more pages than one round of a scan."""
+    rng = random.Random(5)
+    ref = Pool(2600, 6, 20000)
+    g = Gpu(ref, caches=False)
+    for turn in range(3):
+        grow = [rng.choice([0, 1, 100, 130]) for _ in range(2600)]
+        g.extend(grow)
+        bad = ref.extend(grow)
+        ids = rng.sample(range(2600), 900)
+        g.free(ids)
+        ref.free(ids)
+        empty = [b for b in range(2600) if ref.lens[b] == 0]
+        forks = [(rng.choice([b for b in range(50) if b not in empty] or [0]), c) for c in empty[100:]]
+        pairs = g.fork(forks)
+        exp, bad2 = ref.fork(forks)
+        torch.cuda.synchronize()
+        assert pairs.tolist() == [list(p) for p in exp]
+        g.same(ref)
+        g.error(bad + bad2)
+    t, r, pairs, counts = g.compact(inplace=False)
+    n, moves = ref.compact()
+    torch.cuda.synchronize()
+    assert counts.tolist() == [n, len(moves)] and len(moves) > 0
+    assert pairs.tolist()[:len(moves)] == [list(m) for m in moves]
+    assert t.tolist() == ref.table and r.tolist() == ref.refs
+
+
+def test_forks_beyond_one_block_of_threads():
+    ref = Pool(3000, 3, 4000)
+    g = Gpu(ref, caches=False)
+    grow = [70 if b % 2 else 64 for b in range(100)] + [0] * 2900
+    g.extend(grow)
+    ref.extend(grow)
+    forks = [(i % 100, 100 + i) for i in range(2900)]
+    pairs = g.fork(forks)
+    exp, bad = ref.fork(forks)
+    torch.cuda.synchronize()
+    assert pairs.tolist() == [list(p) for p in exp]
+    g.same(ref)
+    g.error(bad)
+
+
+def test_pages_outside_the_pool_are_reported():
+    ref = Pool(4, 3, 8)
+    ref.extend([130, 70, 0, 0])
+    g = Gpu(ref)
+    g.table[0, 1], g.table[1, 1] = 8, -1
+    g.free([0])
+    g.error([0])
+    g.fork([(1, 2)])  # its partly filled page is not in the pool: refused
+    torch.cuda.synchronize()
+    assert g.lens.tolist() == [0, 70, 0, 0]
+    g.error([0])
+    refs = g.refs.clone()
+    g.compact(inplace=False)
+    g.error([1])
+    g.free([3, 9, -1])
+    g.error([1, 2])
+    assert torch.equal(g.refs, refs)
