@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
-        if (lane == 0) {
+        if (elect_one()) {
             int u = 0, boxes = 0;
             for (int x = 0; x < p.products && !*abort_flag; ++x) {
                 const int col = (first + x) * NC % kKv, wrow = (first + x) * NC / kKv * kLatent;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc = idesc_bf16(kApRows, NC, 0, 1);
             const uint64_t a_d0 = smem_desc(smem_u32(smem + SM::oA), 16, 1024, kSw128);
             const uint64_t b_d0 = smem_desc(smem_u32(smem + SM::oB), kApBoxB, 1024, kSw128);

@@ -238,12 +238,10 @@ struct PfIter {
     }
 };
 
-// Ring units: K(s) is three units and precedes V(s - 1), two units, in the order of use
-// (S of step s + 1 is issued before O of step s needs V(s)); V of the last step ends it.
-__device__ __forceinline__ uint32_t k_unit(uint32_t s) { return s == 0 ? 0 : 5 * s - 2; }
-__device__ __forceinline__ uint32_t v_unit(uint32_t s, uint32_t steps) {
-    return s + 1 < steps ? 5 * s + 6 : 5 * s + 3;
-}
+// Ring units of step s, in the order of use: three of K(s), two of V(s). (K(s + 1) before
+// V(s) would keep V(s) out until K(s) is free, just before it is needed.)
+__device__ __forceinline__ uint32_t k_unit(uint32_t s) { return 5 * s; }
+__device__ __forceinline__ uint32_t v_unit(uint32_t s) { return 5 * s + 3; }
 
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_gqa_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap kr_map,
@@ -304,7 +302,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfIssueRegs));
         if (warp == 0) {
             // ------------------------------------------------------------ TMA producer
-            if (lane == 0 && steps > 0) {
+            if (steps > 0 && elect_one()) {
                 uint32_t u = 0, qn[2] = {0, 0};
                 auto unit = [&]() -> uint8_t * {  // the next ring unit, once it is free
                     const uint32_t sl = u % kPfUnits;
@@ -339,8 +337,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 };
                 PfIter it(p, plan);
                 PfPiece pc;
-                Slots prev{0, 0};
-                int prev_g = -1;
                 const uint32_t q_bytes = (uint32_t)(p.tile_tokens * p.G) * 128u;
                 while (!*abort_flag && it.next(p, pc)) {
                     for (int q = 0; q < 2 && q * p.tile_tokens < pc.ntok; ++q) {
@@ -368,12 +364,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                             }
                             ++u;
                         }
-                        if (prev_g >= 0) load_v(prev_g, prev);
-                        prev = sl;
-                        prev_g = pc.g;
+                        if (!*abort_flag) load_v(pc.g, sl);
                     }
                 }
-                if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev);
                 // never leave with copies in flight: wait (bounded) for the last ones issued
                 int dummy = 0;
                 volatile int *no_abort = reinterpret_cast<volatile int *>(&dummy);
@@ -384,7 +377,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
-            if (lane == 0 && steps > 0) {
+            if (steps > 0 && elect_one()) {
                 constexpr uint32_t idesc_s = idesc_bf16(kPfRows, kPfTile, 0, 0);
                 constexpr uint32_t idesc_pv = idesc_bf16(kPfRows, kDv, 0, 1);
                 const uint64_t q_d0 = smem_desc(smem_u32(smem + SM::oQ), 16, 1024, kSw128);
@@ -419,7 +412,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 };
                 // O_q of step s
                 auto product = [&](const PfPiece &pc, int t, uint32_t s, int q, int nq) {
-                    const uint32_t u = v_unit(s, steps);
+                    const uint32_t u = v_unit(s);
                     if (q == 0) {
                         for (int h = 0; h < 2; ++h) wait(&full[(u + h) % kPfUnits], ((u + h) / kPfUnits) & 1);
                         if (t == pc.nt - 1 && pc.kv_end % kPfTile != 0) {
@@ -486,7 +479,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 s += pc.t1 - pc.t0;
                 const int keep = pc.kv_end % kPfTile;
                 if (pc.t1 != pc.nt || keep == 0) continue;
-                const uint32_t u = v_unit(s - 1, steps);
+                const uint32_t u = v_unit(s - 1);
                 bool ok = mbar_wait_long(v_ask, fixes++ & 1, abort_flag);
                 for (int h = 0; h < 2; ++h)
                     ok = ok && mbar_wait(&full[(u + h) % kPfUnits], ((u + h) / kPfUnits) & 1, abort_flag);
