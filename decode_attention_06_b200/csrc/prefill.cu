@@ -243,6 +243,84 @@ struct PfIter {
 __device__ __forceinline__ uint32_t k_unit(uint32_t s) { return 5 * s; }
 __device__ __forceinline__ uint32_t v_unit(uint32_t s) { return 5 * s + 3; }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// 2^x of two values on the FMA pipes: x = n + f with n = round(x), |f| <= 1/2 (Cody-Waite),
+// 2^f by its minimax polynomial of degree 4 (Remez exchange; relative error 2.7e-6, against
+// the 2^-9 of P in bf16), n added to the exponent. For finite x <= 127; below -126 it gives
+// about 2^-126.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: x + kMagic holds round(x) in its low bits
+    x.x = fmaxf(x.x, -126.0f);
+    x.y = fmaxf(x.y, -126.0f);
+    const float2 n = add2(x, make_float2(kMagic, kMagic));
+    const float2 f = add2(x, fma2(n, make_float2(-1.0f, -1.0f), make_float2(kMagic, kMagic)));
+    float2 r = make_float2(0.00957010221f, 0.00957010221f);
+    r = fma2(r, f, make_float2(0.0559178591f, 0.0559178591f));
+    r = fma2(r, f, make_float2(0.240247443f, 0.240247443f));
+    r = fma2(r, f, make_float2(0.693121791f, 0.693121791f));
+    r = fma2(r, f, make_float2(0.999999285f, 0.999999285f));
+    return make_float2(__uint_as_float(__float_as_uint(r.x) + (__float_as_uint(n.x) << 23)),
+                       __uint_as_float(__float_as_uint(r.y) + (__float_as_uint(n.y) << 23)));
+}
+
+// P = 2^(s scale - mu) of a row's 128 scores, rounded to bf16, into the row's P columns;
+// returns the sum of the unrounded values. FAST: also the largest score, and every fourth
+// pair of exponentials on the FMA pipes (the 16 a cycle of the special-function unit bound
+// the loop otherwise); scores must be finite or `mx` NaN says that they were not.
+template <bool FAST>
+__device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, float mu, uint32_t t_p, float &mx) {
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const float2 sc = make_float2(scale, scale), sub = make_float2(-mu, -mu);
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 128; i += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            const float2 s = make_float2(__uint_as_float(sv[i + e]), __uint_as_float(sv[i + e + 1]));
+            const float2 x = fma2(s, sc, sub);
+            float2 v;
+            if (FAST && e % 8 == 6) v = exp2_fma(x);
+            else v = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            if (FAST) top[(e >> 1) & 1] = max_nan(top[(e >> 1) & 1], max_nan(s.x, s.y));
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], v);
+            __nv_bfloat162 h2 = __floats2bfloat162_rn(v.x, v.y);
+            w[e / 2] = *reinterpret_cast<uint32_t *>(&h2);
+        }
+        tmem_st16(t_p + i / 2, w);
+    }
+    mx = max_nan(top[0], top[1]);
+    const float2 t = add2(sum[0], sum[1]);
+    return t.x + t.y;
+}
+
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_gqa_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap kr_map,
                        const __grid_constant__ CUtensorMap q_map, const PfParams p) {
@@ -527,22 +605,35 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32 * i, sv + 32 * i);
                     tmem_wait_ld();
                     const int lim = valid ? last + 1 - t * kPfTile : 0;  // keys of this tile that the row sees
-                    if (__any_sync(0xffffffffu, lim < kPfTile)) {
-#pragma unroll
-                        for (int e = 0; e < 128; ++e)
-                            if (e >= lim) sv[e] = 0xff800000u;
+                    const bool masked = __any_sync(0xffffffffu, lim < kPfTile);
+                    // P against the maximum so far, at once; only where a row's score rose more
+                    // than 2^8 above it (and on a piece's first tile, and under a mask) again
+                    // against the new one. A NaN score takes the second way.
+                    float lt = 0.0f;
+                    bool redo = t == pc.t0 || masked;
+                    if (!redo) {
+                        float mx;
+                        lt = form_p<true>(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_s, mx);
+                        redo = __any_sync(0xffffffffu, !(mx * p.scale_log2 <= m + kPfRescaleLog2));
                     }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (redo) {
+                        if (masked) {
 #pragma unroll
-                    for (int e = 0; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[e]));
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-                    // S of this step complete means O of the step before is: they are issued in order
-                    const bool rise = mt > m + kPfRescaleLog2;
-                    if (__any_sync(0xffffffffu, rise)) {
+                            for (int e = 0; e < 128; ++e)
+                                if (e >= lim) sv[e] = 0xff800000u;
+                        }
+                        float mt = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 128; e += 2)
+                            mt = fmaxf(mt, fmaxf(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])));
+                        mt *= p.scale_log2;
+                        const bool rise = mt > m + kPfRescaleLog2;
                         const float a = rise ? fast_exp2(m - mt) : 1.0f;  // 0 from an empty row
                         if (rise) m = mt;
                         l *= a;
-                        if (t > pc.t0) {
+                        // S of this step complete means O of the step before is: they are issued
+                        // in order
+                        if (t > pc.t0 && __any_sync(0xffffffffu, rise)) {
 #pragma unroll 1
                             for (int i = 0; i < kDv; i += 16) {
                                 uint32_t r[16];
@@ -553,24 +644,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                                 tmem_st16(t_o + i, r);
                             }
                         }
+                        tmem_wait_st();
+                        float mx;
+                        lt = form_p<false>(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_s, mx);
                     }
-                    const float mu = m == -INFINITY ? 0.0f : m;
-                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 128; i += 32) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float p0 = fast_exp2(fmaf(__uint_as_float(sv[i + e]), p.scale_log2, -mu));
-                            const float p1 = fast_exp2(fmaf(__uint_as_float(sv[i + e + 1]), p.scale_log2, -mu));
-                            ls[e & 2] += p0;
-                            ls[(e & 2) + 1] += p1;
-                            __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
-                            w[e / 2] = *reinterpret_cast<uint32_t *>(&h2);
-                        }
-                        tmem_st16(t_s + i / 2, w);
-                    }
-                    l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                    l += lt;
                     tmem_wait_st();
                 }
                 tc_fence_before();
