@@ -47,17 +47,17 @@ static_assert(128 * kPfIssueRegs + 256 * kPfSoftmaxRegs <= kPfThreads * kPfLaunc
 constexpr float kPfRescaleLog2 = 8.0f;
 
 constexpr int kPfBox = 64 * 128;          // one TMA box: 64 rows of 128 bytes
-constexpr int kPfUnit = 2 * kPfBox;       // ring unit
-constexpr int kPfUnits = 8;               // units in the ring
+constexpr int kPfUnit = kPfBox;           // ring unit of one CTA
+constexpr int kPfUnits = 16;              // units in the ring
 constexpr int kPfQBlock = kPfRows * 128;  // 64 columns of a query tile
 
 struct PfSmem {
     static constexpr int oQ = 0;                                   // [2 tiles][3 column blocks]
     static constexpr int oRing = oQ + 6 * kPfQBlock;
     static constexpr int oBar = oRing + kPfUnits * kPfUnit;
-    // full/empty[units], q_full/q_empty[2], s_full[2], p_full[2], o_full/o_free[2], v_ask,
-    // v_fixed, drain
-    static constexpr int kNumBars = 2 * kPfUnits + 4 + 2 + 2 + 4 + 2 + 1;
+    // full/empty[units], q_full/q_empty[2], s_full[2], s_free, p_full[2], pv_done[2], o_free[2],
+    // v_ask, v_fixed, drain
+    static constexpr int kNumBars = 2 * kPfUnits + 4 + 2 + 1 + 2 + 2 + 2 + 2 + 1;
     static constexpr int oPlan = oBar + kNumBars * 8;              // int64 rem; int b, g, i, t
     static constexpr int oMisc = oPlan + 32;                       // tmem base, abort flag
     static constexpr int kBytes = oMisc + 16;
@@ -83,10 +83,11 @@ struct PfParams {
 // Bounded wait of a role that may have nothing to do for whole blocks (a query tile that
 // short blocks leave empty, the V rows of blocks that end on a tile): the roles that feed it
 // give up after kWaitCycles and raise the abort flag; its own limit is 32 times that.
+template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity, volatile int *abort) {
     const long long t0 = clock64();
     while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
         if (clock64() - t0 > 32 * kWaitCycles) return false;
     }
@@ -238,10 +239,20 @@ struct PfIter {
     }
 };
 
-// Ring units of step s, in the order of use: three of K(s), two of V(s). (K(s + 1) before
-// V(s) would keep V(s) out until K(s) is free, just before it is needed.)
-__device__ __forceinline__ uint32_t k_unit(uint32_t s) { return 5 * s; }
-__device__ __forceinline__ uint32_t v_unit(uint32_t s) { return 5 * s + 3; }
+// Ring units, in the order of use: K(s + 1), three units, before V(s), two; V of the last
+// step ends it.
+__device__ __forceinline__ uint32_t k_unit(uint32_t s) { return s == 0 ? 0 : 5 * s - 2; }
+__device__ __forceinline__ uint32_t v_unit(uint32_t s, uint32_t steps) {
+    return s + 1 < steps ? 5 * s + 6 : 5 * s + 3;
+}
+
+// TMEM columns: P of the two query tiles (bf16, 64 columns each) with the one S between
+// them, then O. The tiles take turns with S: it is free again as soon as the softmax has
+// read it, so S of the next step is formed while P of this one still is, and no tile waits
+// for its own P -> O -> S chain.
+constexpr int kPfColS = 64;
+__device__ __forceinline__ uint32_t p_col(int q) { return q ? 192 : 0; }
+__device__ __forceinline__ uint32_t o_col(int q) { return 256 + kDv * q; }
 
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -294,8 +305,9 @@ __device__ __forceinline__ float2 exp2_fma(float2 x) {
 // returns the sum of the unrounded values. FAST: also the largest score, and every fourth
 // pair of exponentials on the FMA pipes (the 16 a cycle of the special-function unit bound
 // the loop otherwise); scores must be finite or `mx` NaN says that they were not.
-template <bool FAST>
-__device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, float mu, uint32_t t_p, float &mx) {
+template <bool FAST, typename Ready>
+__device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, float mu, uint32_t t_p, float &mx,
+                                        Ready ready) {
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float2 sc = make_float2(scale, scale), sub = make_float2(-mu, -mu);
     float top[2] = {-INFINITY, -INFINITY};
@@ -314,6 +326,7 @@ __device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, 
             __nv_bfloat162 h2 = __floats2bfloat162_rn(v.x, v.y);
             w[e / 2] = *reinterpret_cast<uint32_t *>(&h2);
         }
+        if (i == 0) ready();  // P of the step before has been used
         tmem_st16(t_p + i / 2, w);
     }
     mx = max_nan(top[0], top[1]);
@@ -321,7 +334,7 @@ __device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, 
     return t.x + t.y;
 }
 
-__global__ void __launch_bounds__(kPfThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     prefill_gqa_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap kr_map,
                        const __grid_constant__ CUtensorMap q_map, const PfParams p) {
     using SM = PfSmem;
@@ -329,23 +342,28 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + SM::oBar), *empty = full + kPfUnits;
     uint64_t *q_full = empty + kPfUnits, *q_empty = q_full + 2;
-    uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *o_free = o_full + 2;
+    uint64_t *s_full = q_empty + 2, *s_free = s_full + 2, *p_full = s_free + 1, *pv_done = p_full + 2;
+    uint64_t *o_free = pv_done + 2;
     uint64_t *v_ask = o_free + 2, *v_fixed = v_ask + 1, *drain = v_fixed + 1;
     int *plan = reinterpret_cast<int *>(smem + SM::oPlan);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::oMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::oMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x;
+    const int c = blockIdx.x >> 1;  // this pair's chunk
+    const uint32_t rank = cluster_rank();
+    // the barriers that the MMA issuer waits for are those of rank 0
+    auto lead = [](uint64_t *bar) { return map_peer(smem_u32(bar), 0); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPfUnits; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
-            mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4);
-            mbar_init(&o_full[i], 1); mbar_init(&o_free[i], 4);
+            mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8);
+            mbar_init(&pv_done[i], 1); mbar_init(&o_free[i], 8);
         }
+        mbar_init(s_free, 8);
         mbar_init(v_ask, 1);
-        mbar_init(v_fixed, 1);
+        mbar_init(v_fixed, 2);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -354,14 +372,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         prefetch_tensormap(&q_map);
     }
     if (warp == 2) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
         tc_fence_before();
     }
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 0) {
-        const int64_t total = pf_total(p, c == 0);
+        const int64_t total = pf_total(p, blockIdx.x == 0);
         const int64_t k = (total + p.num_splits - 1) / p.num_splits;
         const int64_t r0 = c * k, rem = min(total, r0 + k) - r0;
         PfPlace at{0, 0, 0, 0, 0};
@@ -372,6 +390,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
     }
     __syncthreads();
+    cluster_sync();  // the other CTA's barriers are initialised too
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t steps = (uint32_t)*reinterpret_cast<const int64_t *>(plan);
@@ -386,11 +405,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     const uint32_t sl = u % kPfUnits;
                     if (!mbar_wait(&empty[sl], ((u / kPfUnits) & 1) ^ 1, abort_flag)) *abort_flag = 1;
                     if (*abort_flag) return nullptr;
-                    mbar_arrive_expect_tx(&full[sl], kPfUnit);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[sl], 2 * kPfUnit);  // both CTAs' parts
                     return smem + SM::oRing + sl * kPfUnit;
                 };
-                // first cache slot of the pages of a tile; a missing page reads as zeros
-                // (a row past the end of the map)
+                // first cache slots of the two pages of a tile; a missing page reads as zeros (a
+                // row past the end of the map)
                 struct Slots { int s0, s1; };
                 auto slots = [&](const PfPiece &pc, int t) -> Slots {
                     const int32_t *row = p.page_table + (int64_t)pc.b * p.max_pages;
@@ -401,67 +420,65 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     return Slots{ok0 ? a0 * kPage : (int)p.num_slots,
                                  ok1 && pg + 1 < pages ? a1 * kPage : (int)p.num_slots};
                 };
+                // V: both pages, this CTA's 64 columns
                 auto load_v = [&](int g, const Slots &sl) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint8_t *dst = unit();
                         if (!dst) return;
-                        uint64_t *bar = &full[u % kPfUnits];
-                        const int y = h ? sl.s1 : sl.s0;
-                        tma_load_3d(dst, &kv_map, bar, kNope, y, g);
-                        tma_load_3d(dst + kPfBox, &kv_map, bar, kNope + 64, y, g);
+                        tma_load_3d_pair(dst, &kv_map, lead(&full[u % kPfUnits]), kNope + 64 * (int)rank,
+                                         h ? sl.s1 : sl.s0, g);
                         ++u;
                     }
                 };
                 PfIter it(p, plan);
                 PfPiece pc;
+                Slots prev{0, 0};
+                int prev_g = -1;
                 const uint32_t q_bytes = (uint32_t)(p.tile_tokens * p.G) * 128u;
                 while (!*abort_flag && it.next(p, pc)) {
-                    for (int q = 0; q < 2 && q * p.tile_tokens < pc.ntok; ++q) {
+                    for (int q = 0; q < 2 && 2 * q * p.tile_tokens < pc.ntok; ++q) {
                         if (!mbar_wait(&q_empty[q], (qn[q] & 1) ^ 1, abort_flag)) *abort_flag = 1;
                         if (*abort_flag) break;
                         ++qn[q];
-                        mbar_arrive_expect_tx(&q_full[q], 3 * q_bytes);
-                        for (int cb = 0; cb < 3; ++cb)
-                            tma_load_3d(smem + SM::oQ + (3 * q + cb) * kPfQBlock, &q_map, &q_full[q], 64 * cb,
-                                        pc.g * p.G, (int)(pc.row0 + q * p.tile_tokens));
+                        if (rank == 0) mbar_arrive_expect_tx(&q_full[q], 2 * 3 * q_bytes);
+                        for (int cb = 0; cb < 3; ++cb)  // rows past the batch read as zeros
+                            tma_load_3d_pair(smem + SM::oQ + (3 * q + cb) * kPfQBlock, &q_map, lead(&q_full[q]), 64 * cb,
+                                             pc.g * p.G, (int)(pc.row0 + (2 * q + (int)rank) * p.tile_tokens));
                     }
                     for (int t = pc.t0; t < pc.t1 && !*abort_flag; ++t) {
                         const Slots sl = slots(pc, t);
+                        const int y = rank ? sl.s1 : sl.s0;
 #pragma unroll
-                        for (int cb = 0; cb < 3; ++cb) {  // K_nope lo, hi, RoPE keys: 64 columns x 128 keys
+                        for (int cb = 0; cb < 3; ++cb) {  // K_nope lo, hi, RoPE keys of this CTA's page
                             uint8_t *dst = unit();
                             if (!dst) break;
-                            uint64_t *bar = &full[u % kPfUnits];
-                            if (cb < 2) {
-                                tma_load_3d(dst, &kv_map, bar, 64 * cb, sl.s0, pc.g);
-                                tma_load_3d(dst + kPfBox, &kv_map, bar, 64 * cb, sl.s1, pc.g);
-                            } else {
-                                tma_load_2d(dst, &kr_map, bar, 0, sl.s0);
-                                tma_load_2d(dst + kPfBox, &kr_map, bar, 0, sl.s1);
-                            }
+                            const uint32_t bar = lead(&full[u % kPfUnits]);
+                            if (cb < 2) tma_load_3d_pair(dst, &kv_map, bar, 64 * cb, y, pc.g);
+                            else tma_load_2d_pair(dst, &kr_map, bar, 0, y);
                             ++u;
                         }
-                        if (!*abort_flag) load_v(pc.g, sl);
+                        if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev);
+                        prev = sl;
+                        prev_g = pc.g;
                     }
                 }
-                // never leave with copies in flight: wait (bounded) for the last ones issued
-                int dummy = 0;
-                volatile int *no_abort = reinterpret_cast<volatile int *>(&dummy);
-                for (uint32_t x = (u > kPfUnits ? u - kPfUnits : 0); x < u; ++x)
-                    mbar_wait(&full[x % kPfUnits], (x / kPfUnits) & 1, no_abort);
+                if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev);
+                // every copy has been used, and the other CTA's commits have arrived here
+                for (uint32_t x = (u > kPfUnits ? u - kPfUnits : 0); x < u && !*abort_flag; ++x)
+                    if (!mbar_wait(&empty[x % kPfUnits], (x / kPfUnits) & 1, abort_flag)) *abort_flag = 1;
                 for (int q = 0; q < 2; ++q)
-                    if (qn[q]) mbar_wait(&q_full[q], (qn[q] - 1) & 1, no_abort);
+                    if (qn[q] && !*abort_flag && !mbar_wait(&q_empty[q], (qn[q] - 1) & 1, abort_flag)) *abort_flag = 1;
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
-            if (steps > 0 && elect_one()) {
-                constexpr uint32_t idesc_s = idesc_bf16(kPfRows, kPfTile, 0, 0);
-                constexpr uint32_t idesc_pv = idesc_bf16(kPfRows, kDv, 0, 1);
+            if (rank == 0 && steps > 0 && elect_one()) {
+                constexpr uint32_t idesc_s = idesc_bf16(2 * kPfRows, kPfTile, 0, 0);
+                constexpr uint32_t idesc_pv = idesc_bf16(2 * kPfRows, kDv, 0, 1);
                 const uint64_t q_d0 = smem_desc(smem_u32(smem + SM::oQ), 16, 1024, kSw128);
                 const uint64_t k_d0 = smem_desc(smem_u32(smem + SM::oRing), 16, 1024, kSw128);
                 const uint64_t v_d0 = smem_desc(smem_u32(smem + SM::oRing), kPfBox, 1024, kSw128);
-                uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0}, fixes = 0;
+                uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0}, fixes = 0, sn = 0;
                 auto wait = [&](uint64_t *bar, uint32_t parity) {
                     if (!mbar_wait(bar, parity, abort_flag)) *abort_flag = 1;
                 };
@@ -469,6 +486,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 // the query tile
                 auto score = [&](const PfPiece &pc, int t, uint32_t s, int q, int nq) {
                     if (t == pc.t0) wait(&q_full[q], qn[q]++ & 1);
+                    if (sn++ > 0) wait(s_free, sn & 1);  // the softmax has read the S before this one
                     const uint32_t u = k_unit(s);
 #pragma unroll
                     for (int cb = 0; cb < 3; ++cb) {
@@ -480,22 +498,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                             const uint64_t kd = desc_advance(k_d0, sl * kPfUnit);
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                mma_bf16(tmem + kPfTile * q, desc_advance(qd, ks * 32), desc_advance(kd, ks * 32),
+                                mma_bf16_pair(tmem + kPfColS, desc_advance(qd, ks * 32), desc_advance(kd, ks * 32),
                                          idesc_s, (cb > 0 || ks > 0) ? 1u : 0u);
                         }
-                        if (q == nq - 1) mma_commit(&empty[sl]);
+                        if (q == nq - 1) mma_commit_pair(&empty[sl]);
                     }
-                    mma_commit(&s_full[q]);
-                    if (t == pc.t1 - 1) mma_commit(&q_empty[q]);
+                    mma_commit_pair(&s_full[q]);
+                    if (t == pc.t1 - 1) mma_commit_pair(&q_empty[q]);
                 };
                 // O_q of step s
                 auto product = [&](const PfPiece &pc, int t, uint32_t s, int q, int nq) {
-                    const uint32_t u = v_unit(s);
+                    const uint32_t u = v_unit(s, steps);
                     if (q == 0) {
                         for (int h = 0; h < 2; ++h) wait(&full[(u + h) % kPfUnits], ((u + h) / kPfUnits) & 1);
                         if (t == pc.nt - 1 && pc.kv_end % kPfTile != 0) {
-                            mbar_arrive(v_ask);
-                            wait(v_fixed, fixes++ & 1);
+                            mbar_arrive_remote(map_peer(smem_u32(v_ask), 0));
+                            mbar_arrive_remote(map_peer(smem_u32(v_ask), 1));
+                            if (!mbar_wait_cluster(v_fixed, fixes++ & 1, abort_flag)) *abort_flag = 1;
                         }
                     }
                     if (t == pc.t0) wait(&o_free[q], (on[q]++ & 1) ^ 1);
@@ -508,18 +527,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                             const uint64_t vd = desc_advance(v_d0, sl * kPfUnit);
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                mma_bf16_ts(tmem + 256 + kDv * q, tmem + kPfTile * q + 32 * h + 8 * ks,
+                                mma_bf16_ts_pair(tmem + o_col(q), tmem + p_col(q) + 32 * h + 8 * ks,
                                             desc_advance(vd, ks * 2048), idesc_pv,
                                             (t > pc.t0 || h > 0 || ks > 0) ? 1u : 0u);
                         }
-                        if (q == nq - 1) mma_commit(&empty[sl]);
+                        if (q == nq - 1) mma_commit_pair(&empty[sl]);
                     }
-                    if (t == pc.t1 - 1) mma_commit(&o_full[q]);
+                    mma_commit_pair(&pv_done[q]);
                 };
                 PfIter it(p, plan);
                 PfPiece pc, nx;
                 it.next(p, pc);
-                int t = pc.t0, nq = pc.ntok > p.tile_tokens ? 2 : 1;
+                int t = pc.t0, nq = pc.ntok > 2 * p.tile_tokens ? 2 : 1;
                 for (int q = 0; q < nq; ++q) score(pc, t, 0, q, nq);
                 for (uint32_t s = 0; s < steps && !*abort_flag; ++s) {
                     // the step after this one
@@ -529,18 +548,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     if (nt == pc.t1) {
                         more = it.next(p, nx);
                         nt = nx.t0;
-                        nnq = nx.ntok > p.tile_tokens ? 2 : 1;
+                        nnq = nx.ntok > 2 * p.tile_tokens ? 2 : 1;
                     }
                     for (int q = 0; q < 2; ++q) {
-                        if (q < nq) product(pc, t, s, q, nq);
                         if (more && q < nnq) score(nx, nt, s + 1, q, nnq);
+                        if (q < nq) product(pc, t, s, q, nq);
                     }
                     pc = nx;
                     t = nt;
                     nq = nnq;
                 }
                 // nothing may still be running when TMEM is freed
-                mma_commit(drain);
+                mma_commit_pair(drain, 1);
                 int dummy = 0;
                 mbar_wait(drain, 0, reinterpret_cast<volatile int *>(&dummy));
             }
@@ -557,22 +576,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 s += pc.t1 - pc.t0;
                 const int keep = pc.kv_end % kPfTile;
                 if (pc.t1 != pc.nt || keep == 0) continue;
-                const uint32_t u = v_unit(s - 1);
-                bool ok = mbar_wait_long(v_ask, fixes++ & 1, abort_flag);
-                for (int h = 0; h < 2; ++h)
-                    ok = ok && mbar_wait(&full[(u + h) % kPfUnits], ((u + h) / kPfUnits) & 1, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                const uint32_t u = v_unit(s - 1, steps);
+                if (!__all_sync(0xffffffffu, mbar_wait_long<true>(v_ask, fixes++ & 1, abort_flag))) break;
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t sl = (u + h) % kPfUnits;
-                    uint8_t *v = smem + SM::oRing + sl * kPfUnit;
+                    uint8_t *v = smem + SM::oRing + (u + h) % kPfUnits * kPfUnit;
                     const int r0 = min(max(keep - kPage * h, 0), kPage);  // first row to clear in this page
-                    for (int i = lane; i < (kPage - r0) * 16; i += 32)
-                        *reinterpret_cast<uint4 *>(v + (i & 1) * kPfBox + (r0 + (i >> 4)) * 128 + ((i >> 1) & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
+                    for (int i = lane; i < (kPage - r0) * 8; i += 32)
+                        *reinterpret_cast<uint4 *>(v + r0 * 128 + i * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(v_fixed);
+                if (lane == 0) mbar_arrive_remote(lead(v_fixed));
             }
         }
         // warp 2 owns TMEM and is otherwise idle
@@ -582,21 +596,29 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int q = (warp - 4) >> 2;             // query tile
         const int row = 32 * (warp & 3) + lane;    // this thread's query row: its TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t t_s = tmem + kPfTile * q + lane_off, t_o = tmem + 256 + kDv * q + lane_off;
-        const int tok = q * p.tile_tokens + row / p.G, hg = row % p.G;  // token of the block, head of the group
+        const uint32_t t_s = tmem + kPfColS + lane_off, t_p = tmem + p_col(q) + lane_off, t_o = tmem + o_col(q) + lane_off;
+        const int tok = (2 * q + (int)rank) * p.tile_tokens + row / p.G, hg = row % p.G;  // token of the block, head of the group
         const bool in_tile = row < p.tile_tokens * p.G;
-        uint32_t sn = 0, on = 0;
+        uint32_t sn = 0, pvn = 0;  // steps seen, and products of this tile known to be complete
         PfIter it(p, plan);
         PfPiece pc;
         bool alive = true;  // the same in all lanes of the warp
+        // the first n products of this tile are complete: P may be written, O changed or read
+        auto products = [&](uint32_t n) {
+            if (pvn < n) {
+                alive = __all_sync(0xffffffffu, mbar_wait(&pv_done[q], pvn & 1, abort_flag)) && alive;
+                tc_fence_after();
+                ++pvn;
+            }
+        };
         while (alive && it.next(p, pc)) {
-            if (q * p.tile_tokens >= pc.ntok) continue;
+            if (2 * q * p.tile_tokens >= pc.ntok) continue;
             const bool valid = in_tile && tok < pc.ntok;
             const bool warp_valid = __any_sync(0xffffffffu, valid);
             const int last = pc.pos0 + tok;   // the last key this row sees
             float m = -INFINITY, l = 0.0f;    // maximum (log2 units) and sum of this row
             for (int t = pc.t0; t < pc.t1; ++t) {
-                alive = __all_sync(0xffffffffu, mbar_wait_long(&s_full[q], sn++ & 1, abort_flag));
+                alive = __all_sync(0xffffffffu, mbar_wait_long<false>(&s_full[q], sn++ & 1, abort_flag)) && alive;
                 if (!alive) break;
                 tc_fence_after();
                 if (warp_valid) {
@@ -604,6 +626,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32 * i, sv + 32 * i);
                     tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote_relaxed(lead(s_free));
                     const int lim = valid ? last + 1 - t * kPfTile : 0;  // keys of this tile that the row sees
                     const bool masked = __any_sync(0xffffffffu, lim < kPfTile);
                     // P against the maximum so far, at once; only where a row's score rose more
@@ -613,7 +638,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     bool redo = t == pc.t0 || masked;
                     if (!redo) {
                         float mx;
-                        lt = form_p<true>(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_s, mx);
+                        lt = form_p<true>(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_p, mx, [&] { products(sn - 1); });
                         redo = __any_sync(0xffffffffu, !(mx * p.scale_log2 <= m + kPfRescaleLog2));
                     }
                     if (redo) {
@@ -631,8 +656,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         const float a = rise ? fast_exp2(m - mt) : 1.0f;  // 0 from an empty row
                         if (rise) m = mt;
                         l *= a;
-                        // S of this step complete means O of the step before is: they are issued
-                        // in order
+                        products(sn - 1);
                         if (t > pc.t0 && __any_sync(0xffffffffu, rise)) {
 #pragma unroll 1
                             for (int i = 0; i < kDv; i += 16) {
@@ -646,23 +670,27 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         }
                         tmem_wait_st();
                         float mx;
-                        lt = form_p<false>(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_s, mx);
+                        lt = form_p<false>(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_p, mx, [] {});
                     }
                     l += lt;
                     tmem_wait_st();
+                } else {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote_relaxed(lead(s_free));
+                    products(sn - 1);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[q]);
+                if (lane == 0) mbar_arrive_remote_relaxed(lead(&p_full[q]));
             }
             // ---- epilogue: O / l and the LSE, to the output or to this piece's partial
-            alive = alive && __all_sync(0xffffffffu, mbar_wait(&o_full[q], on++ & 1, abort_flag));
+            if (alive) products(sn - 1);
+            if (alive) products(sn);
             if (!alive) break;
-            tc_fence_after();
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             const float lse = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
             const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
-            const int64_t prow = (int64_t)(2 * c + (pc.t0 == 0 ? 1 : 0)) * kPfBlockRows + q * kPfRows + row;
+            const int64_t prow = (int64_t)(2 * c + (pc.t0 == 0 ? 1 : 0)) * kPfBlockRows + (2 * q + (int)rank) * kPfRows + row;
             const int64_t orow = (pc.row0 + tok) * p.heads + pc.g * p.G + hg;
             if (warp_valid) {
                 if (valid) {
@@ -696,16 +724,29 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&o_free[q]);
+            if (lane == 0) mbar_arrive_remote_relaxed(lead(&o_free[q]));
         }
         if (!alive) *abort_flag = 1;
     }
 
+    // Leave together: a CTA that gave up tells the other one; after the first barrier none
+    // sends anything new, and if either gave up both wait until what is in flight (loads,
+    // commits: microseconds) has landed.
+    tc_fence_before();
     __syncthreads();
-    if (*abort_flag && threadIdx.x == 0) report_error(p.ws, GQLA_ERR_TIMEOUT, c);
+    if (threadIdx.x == 0 && *abort_flag) {
+        report_error(p.ws, GQLA_ERR_TIMEOUT, c);
+        st_cluster_b32(map_peer(smem_u32(const_cast<int *>(abort_flag)), rank ^ 1), 1);
+    }
+    cluster_sync();
+    if (*abort_flag) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 200000) {}
+    }
+    cluster_sync();
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 
@@ -836,7 +877,7 @@ cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_
     e = cudaFuncGetAttributes(&fa, prefill_gqa_kernel);
     if (e != cudaSuccess) return e;
     if (128 * kPfIssueRegs + 256 * kPfSoftmaxRegs > kPfThreads * fa.numRegs) return cudaErrorInvalidConfiguration;
-    e = launch_dependent(prefill_gqa_kernel, dim3(num_splits), dim3(kPfThreads), PfSmem::kAlloc, stream, kvm, krm, qm, p);
+    e = launch_dependent(prefill_gqa_kernel, dim3(2 * num_splits), dim3(kPfThreads), PfSmem::kAlloc, stream, kvm, krm, qm, p);
     if (e != cudaSuccess || num_splits == 1) return e;
     return launch_dependent(prefill_combine_kernel, dim3(num_splits - 1, kPfBlockRows / kPcRows),
                             dim3(32 * kPcWarps), 0, stream, p);

@@ -2,13 +2,13 @@
 // kernels and by the host-side planner.
 //
 // Sequence b brings n_b new tokens, the last n_b of its L_b cached ones. A query block
-// is kBlockRows / G tokens of one sequence (times the G heads of one group: two 128-row
-// MMA tiles); its keys are the tokens [0, kv_end), kv_end = the position after its last
+// is 4 (128 / G) tokens of one sequence (times the G heads of one group: two 256-row MMA
+// tiles over a CTA pair); its keys are the tokens [0, kv_end), kv_end = the position after its last
 // token, in tiles of 128. The batch's (block, key tile) pairs, ordered by sequence, group,
 // block and tile, are cut into `num_splits` chunks of ceil(T / num_splits) pairs, one per
-// CTA: every CTA gets the same number of tiles although causal blocks differ in length,
-// and a few rows against a long context spread over many CTAs by the same rule. A block
-// that falls in one chunk is finished by its CTA; of one that a chunk boundary cuts, each
+// CTA pair: every pair gets the same number of tiles although causal blocks differ in length,
+// and a few rows against a long context spread over many pairs by the same rule. A block
+// that falls in one chunk is finished by its pair; of one that a chunk boundary cuts, each
 // piece writes a partial (slot 2c: the block began in an earlier chunk; slot 2c + 1: it
 // begins in chunk c and goes on), merged by the combine.
 #pragma once
@@ -18,12 +18,12 @@
 namespace gqla {
 
 constexpr int kPfTile = 128;        // keys per tile (two pages)
-constexpr int kPfRows = 128;        // query rows of one MMA tile
-constexpr int kPfBlockRows = 256;   // query rows of a block: two MMA tiles
+constexpr int kPfRows = 128;        // query rows of one CTA in an MMA tile
+constexpr int kPfBlockRows = 512;   // query rows of a block: two MMA tiles over two CTAs
 
-// Query tokens of one MMA tile / of a block, for G heads per group.
+// Query tokens of a CTA's part of an MMA tile / of a block, for G heads per group.
 __host__ __device__ inline int pf_tile_tokens(int G) { return kPfRows / G; }
-__host__ __device__ inline int pf_block_tokens(int G) { return 2 * (kPfRows / G); }
+__host__ __device__ inline int pf_block_tokens(int G) { return 4 * (kPfRows / G); }
 
 // sum over i in [0, n) of floor((a i + b) / m), a, b >= 0: the lattice points under a line,
 // by Euclid's steps on (a, m).

@@ -26,7 +26,7 @@ _lib = ctypes.CDLL(_LIB_PATH)
 D_LATENT, D_ROPE, D_NOPE, D_V = 512, 64, 128, 128
 D_QK, D_ROW = D_NOPE + D_ROPE, D_LATENT + D_ROPE
 PAGE_SIZE = 64
-PREFILL_BLOCK_ROWS = 256  # query rows of a partial of gqla_prefill_gqa
+PREFILL_BLOCK_ROWS = 512  # query rows of a partial of gqla_prefill_gqa
 
 STATUS = {0: "GQLA_OK", -1: "GQLA_ERR_INVALID_ARG", -2: "GQLA_ERR_UNSUPPORTED",
           -3: "GQLA_ERR_WORKSPACE", -4: "GQLA_ERR_CUDA", -5: "GQLA_ERR_DEVICE",
@@ -436,8 +436,8 @@ def gqla_plan_prefill(dims, new_tokens, seqlens, max_splits: int) -> int:
 
 
 def plan_prefill(dims, new_tokens, seqlens) -> int:
-    """gqla_plan_prefill up to one CTA for each SM of the current device."""
-    return gqla_plan_prefill(dims, new_tokens, seqlens, gqla_num_splits_hint("gqa", dims.num_heads, 1))
+    """gqla_plan_prefill up to one CTA pair for every two SMs of the current device."""
+    return gqla_plan_prefill(dims, new_tokens, seqlens, max(1, gqla_num_splits_hint("gqa", dims.num_heads, 1) // 2))
 
 
 def gqla_partial_slots(batch: int, num_splits: int) -> int:
