@@ -20,8 +20,7 @@
 //    query row per thread (no exchange between threads), fp32 online softmax in the base-2
 //    domain with lazy rescaling (O is touched only when a row's maximum rises by more than
 //    2^8).
-//  * K and V pass through one ring of eight 16 KB units (K: 64 columns x 128 keys, three to
-//    a tile; V: 64 keys x 128 columns, two to a tile), in the order of use.
+//  * K and V tiles pass through rings of three stages each.
 //  * Work split: prefill_plan.cuh. Every CTA derives its chunk from the device-resident
 //    lengths.
 //  * Every wait is bounded; a wait that runs out records GQLA_ERR_TIMEOUT and the CTA
@@ -47,17 +46,19 @@ static_assert(128 * kPfIssueRegs + 256 * kPfSoftmaxRegs <= kPfThreads * kPfLaunc
 constexpr float kPfRescaleLog2 = 8.0f;
 
 constexpr int kPfBox = 64 * 128;          // one TMA box: 64 rows of 128 bytes
-constexpr int kPfUnit = kPfBox;           // ring unit of one CTA
-constexpr int kPfUnits = 16;              // units in the ring
+constexpr int kPfK = 3 * kPfBox;          // a key tile's K in one CTA: its page's 64 keys x 192
+constexpr int kPfV = 2 * kPfBox;          // and V: 128 keys x its 64 columns
+constexpr int kPfStages = 3;              // tiles in the rings
 constexpr int kPfQBlock = kPfRows * 128;  // 64 columns of a query tile
 
 struct PfSmem {
     static constexpr int oQ = 0;                                   // [2 tiles][3 column blocks]
-    static constexpr int oRing = oQ + 6 * kPfQBlock;
-    static constexpr int oBar = oRing + kPfUnits * kPfUnit;
-    // full/empty[units], q_full/q_empty[2], s_full[2], s_free, p_full[2], pv_done[2], o_free[2],
-    // v_ask, v_fixed, drain
-    static constexpr int kNumBars = 2 * kPfUnits + 4 + 2 + 1 + 2 + 2 + 2 + 2 + 1;
+    static constexpr int oK = oQ + 6 * kPfQBlock;                  // [stages]
+    static constexpr int oV = oK + kPfStages * kPfK;               // [stages]
+    static constexpr int oBar = oV + kPfStages * kPfV;
+    // k_full/k_empty, v_full/v_empty[stages], q_full/q_empty[2], s_full[2], s_free, p_full[2],
+    // pv_done[2], o_free[2], v_ask, v_fixed, drain
+    static constexpr int kNumBars = 4 * kPfStages + 4 + 2 + 1 + 2 + 2 + 2 + 2 + 1;
     static constexpr int oPlan = oBar + kNumBars * 8;              // int64 rem; int b, g, i, t
     static constexpr int oMisc = oPlan + 32;                       // tmem base, abort flag
     static constexpr int kBytes = oMisc + 16;
@@ -239,13 +240,6 @@ struct PfIter {
     }
 };
 
-// Ring units, in the order of use: K(s + 1), three units, before V(s), two; V of the last
-// step ends it.
-__device__ __forceinline__ uint32_t k_unit(uint32_t s) { return s == 0 ? 0 : 5 * s - 2; }
-__device__ __forceinline__ uint32_t v_unit(uint32_t s, uint32_t steps) {
-    return s + 1 < steps ? 5 * s + 6 : 5 * s + 3;
-}
-
 // TMEM columns: P of the two query tiles (bf16, 64 columns each) with the one S between
 // them, then O. The tiles take turns with S: it is free again as soon as the softmax has
 // read it, so S of the next step is formed while P of this one still is, and no tile waits
@@ -279,6 +273,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -321,7 +321,7 @@ __device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, 
             float2 v;
             if (FAST && e % 8 == 6) v = exp2_fma(x);
             else v = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            if (FAST) top[(e >> 1) & 1] = max_nan(top[(e >> 1) & 1], max_nan(s.x, s.y));
+            if (FAST) top[(e >> 1) & 1] = max3_nan(top[(e >> 1) & 1], s.x, s.y);
             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], v);
             __nv_bfloat162 h2 = __floats2bfloat162_rn(v.x, v.y);
             w[e / 2] = *reinterpret_cast<uint32_t *>(&h2);
@@ -340,8 +340,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     using SM = PfSmem;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + SM::oBar), *empty = full + kPfUnits;
-    uint64_t *q_full = empty + kPfUnits, *q_empty = q_full + 2;
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + SM::oBar), *k_empty = k_full + kPfStages;
+    uint64_t *v_full = k_empty + kPfStages, *v_empty = v_full + kPfStages;
+    uint64_t *q_full = v_empty + kPfStages, *q_empty = q_full + 2;
     uint64_t *s_full = q_empty + 2, *s_free = s_full + 2, *p_full = s_free + 1, *pv_done = p_full + 2;
     uint64_t *o_free = pv_done + 2;
     uint64_t *v_ask = o_free + 2, *v_fixed = v_ask + 1, *drain = v_fixed + 1;
@@ -355,7 +356,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     auto lead = [](uint64_t *bar) { return map_peer(smem_u32(bar), 0); };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kPfUnits; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < kPfStages; ++i) {
+            mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8);
@@ -400,13 +404,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         if (warp == 0) {
             // ------------------------------------------------------------ TMA producer
             if (steps > 0 && elect_one()) {
-                uint32_t u = 0, qn[2] = {0, 0};
-                auto unit = [&]() -> uint8_t * {  // the next ring unit, once it is free
-                    const uint32_t sl = u % kPfUnits;
-                    if (!mbar_wait(&empty[sl], ((u / kPfUnits) & 1) ^ 1, abort_flag)) *abort_flag = 1;
-                    if (*abort_flag) return nullptr;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[sl], 2 * kPfUnit);  // both CTAs' parts
-                    return smem + SM::oRing + sl * kPfUnit;
+                uint32_t kn = 0, vn = 0, qn[2] = {0, 0};
+                // the next stage of a ring, once it is free
+                auto stage = [&](uint64_t *fullb, uint64_t *emptyb, uint32_t n, uint32_t bytes) -> int {
+                    const int st = n % kPfStages;
+                    if (!mbar_wait(&emptyb[st], ((n / kPfStages) & 1) ^ 1, abort_flag)) *abort_flag = 1;
+                    if (*abort_flag) return -1;
+                    if (rank == 0) mbar_arrive_expect_tx(&fullb[st], 2 * bytes);  // both CTAs' parts
+                    return st;
                 };
                 // first cache slots of the two pages of a tile; a missing page reads as zeros (a
                 // row past the end of the map)
@@ -422,14 +427,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 };
                 // V: both pages, this CTA's 64 columns
                 auto load_v = [&](int g, const Slots &sl) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint8_t *dst = unit();
-                        if (!dst) return;
-                        tma_load_3d_pair(dst, &kv_map, lead(&full[u % kPfUnits]), kNope + 64 * (int)rank,
-                                         h ? sl.s1 : sl.s0, g);
-                        ++u;
-                    }
+                    const int st = stage(v_full, v_empty, vn, kPfV);
+                    if (st < 0) return;
+                    uint8_t *dst = smem + SM::oV + st * kPfV;
+                    const uint32_t bar = lead(&v_full[st]);
+                    tma_load_3d_pair(dst, &kv_map, bar, kNope + 64 * (int)rank, sl.s0, g);
+                    tma_load_3d_pair(dst + kPfBox, &kv_map, bar, kNope + 64 * (int)rank, sl.s1, g);
+                    ++vn;
                 };
                 PfIter it(p, plan);
                 PfPiece pc;
@@ -449,15 +453,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     for (int t = pc.t0; t < pc.t1 && !*abort_flag; ++t) {
                         const Slots sl = slots(pc, t);
                         const int y = rank ? sl.s1 : sl.s0;
-#pragma unroll
-                        for (int cb = 0; cb < 3; ++cb) {  // K_nope lo, hi, RoPE keys of this CTA's page
-                            uint8_t *dst = unit();
-                            if (!dst) break;
-                            const uint32_t bar = lead(&full[u % kPfUnits]);
-                            if (cb < 2) tma_load_3d_pair(dst, &kv_map, bar, 64 * cb, y, pc.g);
-                            else tma_load_2d_pair(dst, &kr_map, bar, 0, y);
-                            ++u;
-                        }
+                        const int st = stage(k_full, k_empty, kn, kPfK);
+                        if (st < 0) break;
+                        uint8_t *dst = smem + SM::oK + st * kPfK;  // K_nope, RoPE keys of this CTA's page
+                        const uint32_t bar = lead(&k_full[st]);
+                        tma_load_3d_pair(dst, &kv_map, bar, 0, y, pc.g);
+                        tma_load_3d_pair(dst + kPfBox, &kv_map, bar, 64, y, pc.g);
+                        tma_load_2d_pair(dst + 2 * kPfBox, &kr_map, bar, 0, y);
+                        ++kn;
                         if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev);
                         prev = sl;
                         prev_g = pc.g;
@@ -465,8 +468,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 }
                 if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev);
                 // every copy has been used, and the other CTA's commits have arrived here
-                for (uint32_t x = (u > kPfUnits ? u - kPfUnits : 0); x < u && !*abort_flag; ++x)
-                    if (!mbar_wait(&empty[x % kPfUnits], (x / kPfUnits) & 1, abort_flag)) *abort_flag = 1;
+                auto drained = [&](uint64_t *emptyb, uint32_t n) {
+                    for (uint32_t x = (n > kPfStages ? n - kPfStages : 0); x < n && !*abort_flag; ++x)
+                        if (!mbar_wait(&emptyb[x % kPfStages], (x / kPfStages) & 1, abort_flag)) *abort_flag = 1;
+                };
+                drained(k_empty, kn);
+                drained(v_empty, vn);
                 for (int q = 0; q < 2; ++q)
                     if (qn[q] && !*abort_flag && !mbar_wait(&q_empty[q], (qn[q] - 1) & 1, abort_flag)) *abort_flag = 1;
             }
@@ -475,42 +482,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             if (rank == 0 && steps > 0 && elect_one()) {
                 constexpr uint32_t idesc_s = idesc_bf16(2 * kPfRows, kPfTile, 0, 0);
                 constexpr uint32_t idesc_pv = idesc_bf16(2 * kPfRows, kDv, 0, 1);
-                const uint64_t q_d0 = smem_desc(smem_u32(smem + SM::oQ), 16, 1024, kSw128);
-                const uint64_t k_d0 = smem_desc(smem_u32(smem + SM::oRing), 16, 1024, kSw128);
-                const uint64_t v_d0 = smem_desc(smem_u32(smem + SM::oRing), kPfBox, 1024, kSw128);
+                // descriptor words: q and K K-major, V MN-major, all 128-byte swizzled rows
+                const uint64_t q_d = smem_desc(smem_u32(smem + SM::oQ), 16, 1024, kSw128);
+                const uint32_t hi = static_cast<uint32_t>(q_d >> 32), q_lo = static_cast<uint32_t>(q_d);
+                const uint32_t k_lo0 = static_cast<uint32_t>(smem_desc(smem_u32(smem + SM::oK), 16, 1024, kSw128));
+                const uint32_t v_lo0 = static_cast<uint32_t>(smem_desc(smem_u32(smem + SM::oV), 16, 1024, kSw128));
                 uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0}, fixes = 0, sn = 0;
                 auto wait = [&](uint64_t *bar, uint32_t parity) {
                     if (!mbar_wait(bar, parity, abort_flag)) *abort_flag = 1;
                 };
-                // S_q of step s; the step's last query tile frees the K units, a piece's last step
-                // the query tile
+                // S_q of step s; the step's last query tile frees K, a piece's last step the query tile
                 auto score = [&](const PfPiece &pc, int t, uint32_t s, int q, int nq) {
                     if (t == pc.t0) wait(&q_full[q], qn[q]++ & 1);
+                    const int st = s % kPfStages;
+                    if (q == 0) wait(&k_full[st], (s / kPfStages) & 1);
                     if (sn++ > 0) wait(s_free, sn & 1);  // the softmax has read the S before this one
-                    const uint32_t u = k_unit(s);
+                    tc_fence_after();
+                    const uint32_t a = q_lo + q * (3 * kPfQBlock >> 4), b = k_lo0 + st * (kPfK >> 4);
 #pragma unroll
-                    for (int cb = 0; cb < 3; ++cb) {
-                        const uint32_t sl = (u + cb) % kPfUnits;
-                        if (q == 0) wait(&full[sl], ((u + cb) / kPfUnits) & 1);
-                        tc_fence_after();
-                        if (!*abort_flag) {
-                            const uint64_t qd = desc_advance(q_d0, (3 * q + cb) * kPfQBlock);
-                            const uint64_t kd = desc_advance(k_d0, sl * kPfUnit);
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_bf16_pair(tmem + kPfColS, desc_advance(qd, ks * 32), desc_advance(kd, ks * 32),
-                                         idesc_s, (cb > 0 || ks > 0) ? 1u : 0u);
-                        }
-                        if (q == nq - 1) mma_commit_pair(&empty[sl]);
-                    }
+                    for (int ks = 0; ks < 12; ++ks)
+                        mma_bf16_pair(tmem + kPfColS, a + ((ks >> 2) * kPfQBlock + (ks & 3) * 32 >> 4),
+                                      b + ((ks >> 2) * kPfBox + (ks & 3) * 32 >> 4), hi, idesc_s, ks > 0 ? 1u : 0u);
                     mma_commit_pair(&s_full[q]);
+                    if (q == nq - 1) mma_commit_pair(&k_empty[st]);
                     if (t == pc.t1 - 1) mma_commit_pair(&q_empty[q]);
                 };
                 // O_q of step s
                 auto product = [&](const PfPiece &pc, int t, uint32_t s, int q, int nq) {
-                    const uint32_t u = v_unit(s, steps);
+                    const int st = s % kPfStages;
                     if (q == 0) {
-                        for (int h = 0; h < 2; ++h) wait(&full[(u + h) % kPfUnits], ((u + h) / kPfUnits) & 1);
+                        wait(&v_full[st], (s / kPfStages) & 1);
                         if (t == pc.nt - 1 && pc.kv_end % kPfTile != 0) {
                             mbar_arrive_remote(map_peer(smem_u32(v_ask), 0));
                             mbar_arrive_remote(map_peer(smem_u32(v_ask), 1));
@@ -520,20 +521,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     if (t == pc.t0) wait(&o_free[q], (on[q]++ & 1) ^ 1);
                     wait(&p_full[q], pn[q]++ & 1);
                     tc_fence_after();
+                    const uint32_t b = v_lo0 + st * (kPfV >> 4);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t sl = (u + h) % kPfUnits;
-                        if (!*abort_flag) {
-                            const uint64_t vd = desc_advance(v_d0, sl * kPfUnit);
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_bf16_ts_pair(tmem + o_col(q), tmem + p_col(q) + 32 * h + 8 * ks,
-                                            desc_advance(vd, ks * 2048), idesc_pv,
-                                            (t > pc.t0 || h > 0 || ks > 0) ? 1u : 0u);
-                        }
-                        if (q == nq - 1) mma_commit_pair(&empty[sl]);
-                    }
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_bf16_ts_pair(tmem + o_col(q), tmem + p_col(q) + 8 * ks, b + (ks * 2048 >> 4), hi, idesc_pv,
+                                         (ks > 0 || t > pc.t0) ? 1u : 0u);
                     mma_commit_pair(&pv_done[q]);
+                    if (q == nq - 1) mma_commit_pair(&v_empty[st]);
                 };
                 PfIter it(p, plan);
                 PfPiece pc, nx;
@@ -550,6 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                         nt = nx.t0;
                         nnq = nx.ntok > 2 * p.tile_tokens ? 2 : 1;
                     }
+#pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         if (more && q < nnq) score(nx, nt, s + 1, q, nnq);
                         if (q < nq) product(pc, t, s, q, nq);
@@ -576,10 +571,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 s += pc.t1 - pc.t0;
                 const int keep = pc.kv_end % kPfTile;
                 if (pc.t1 != pc.nt || keep == 0) continue;
-                const uint32_t u = v_unit(s - 1, steps);
                 if (!__all_sync(0xffffffffu, mbar_wait_long<true>(v_ask, fixes++ & 1, abort_flag))) break;
                 for (int h = 0; h < 2; ++h) {
-                    uint8_t *v = smem + SM::oRing + (u + h) % kPfUnits * kPfUnit;
+                    uint8_t *v = smem + SM::oV + (s - 1) % kPfStages * kPfV + h * kPfBox;
                     const int r0 = min(max(keep - kPage * h, 0), kPage);  // first row to clear in this page
                     for (int i = lane; i < (kPage - r0) * 8; i += 32)
                         *reinterpret_cast<uint4 *>(v + r0 * 128 + i * 16) = make_uint4(0, 0, 0, 0);
