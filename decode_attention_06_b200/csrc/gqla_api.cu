@@ -478,7 +478,7 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
 
 int gqla_prefill_slots(int num_splits) {
     if (num_splits <= 0 || num_splits > 65535) return GQLA_ERR_INVALID_ARG;
-    return 2 * num_splits;
+    return 2 * num_splits + (num_splits + 127) / 128;  // the last ones: 16-byte merge records
 }
 
 int gqla_plan_prefill(const gqla_dims *dims, const int32_t *new_tokens, const int32_t *seqlens, int batch,
@@ -487,12 +487,12 @@ int gqla_plan_prefill(const gqla_dims *dims, const int32_t *new_tokens, const in
     if (st != GQLA_OK) return st;
     if (!new_tokens || !seqlens || batch <= 0 || batch > 65535 || max_splits <= 0 || max_splits > 65535)
         return GQLA_ERR_INVALID_ARG;
-    const int W = pf_block_tokens(dims->num_heads / dims->num_groups);
+    const int T = pf_tile_tokens(dims->num_heads / dims->num_groups);
     int64_t total = 0;
     for (int b = 0; b < batch; ++b) {
         if (new_tokens[b] < 0 || seqlens[b] < new_tokens[b]) return GQLA_ERR_INVALID_ARG;
         if (new_tokens[b] > 0)
-            total += dims->num_groups * pf_tiles_before(new_tokens[b], seqlens[b], W, pf_blocks(new_tokens[b], W));
+            total += dims->num_groups * pf_units_before(new_tokens[b], seqlens[b], T, pf_blocks(new_tokens[b], T));
     }
     return (int)std::max<int64_t>(1, std::min<int64_t>(max_splits, total));
 }
@@ -509,7 +509,7 @@ int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, cons
     if (!q || !q_starts || !kv_expanded || !k_rope || !out) return GQLA_ERR_INVALID_ARG;
     if (num_splits > 1 && (!o_part || !lse_part)) return GQLA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kv_expanded) || !aligned16(k_rope) || !aligned16(out) ||
-        (o_part && !aligned16(o_part)))
+        (num_splits > 1 && (!aligned16(o_part) || !aligned16(lse_part))))
         return GQLA_ERR_INVALID_ARG;
     if (num_slots != (int64_t)kv->num_pages * kv->page_size) return GQLA_ERR_INVALID_ARG;
     const int64_t most = ((int64_t)1 << 31) - 1;

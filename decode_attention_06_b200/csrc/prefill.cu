@@ -15,11 +15,11 @@
 //      O[128 x 128]  += P (128 x 128, bf16 in TMEM over S) x V (128 x 128, smem, MN-major)
 //    S0, S1, O0, O1 take the 512 TMEM columns. While one tile's softmax runs, the other
 //    tile's products do.
-//  * 12 warps: warp 0 TMA producer, warp 1 MMA issuer, warp 2 TMEM owner, warp 3 clears V
-//    rows past a block's last key; warps 4-7 and 8-11 the softmax of tile 0 and tile 1, one
-//    query row per thread (no exchange between threads), fp32 online softmax in the base-2
-//    domain with lazy rescaling (O is touched only when a row's maximum rises by more than
-//    2^8).
+//  * 12 warps: warp 0 TMA producer, warps 1 and 2 the issuers of S and of O, warp 3 TMEM owner
+//    and clears V rows past a block's last key; warps 4-7 and 8-11 the softmax of tile 0 and
+//    tile 1, one query row per thread (no exchange between threads), fp32 online softmax in the
+//    base-2 domain with lazy rescaling (O is touched only when a row's maximum rises by more
+//    than 2^8).
 //  * K and V tiles pass through rings of three stages each.
 //  * Work split: prefill_plan.cuh. Every CTA derives its chunk from the device-resident
 //    lengths.
@@ -57,10 +57,12 @@ struct PfSmem {
     static constexpr int oV = oK + kPfStages * kPfK;               // [stages]
     static constexpr int oBar = oV + kPfStages * kPfV;
     // k_full/k_empty, v_full/v_empty[stages], q_full/q_empty[2], s_full[2], s_free, p_full[2],
-    // pv_done[2], o_free[2], v_ask, v_fixed, drain
-    static constexpr int kNumBars = 4 * kPfStages + 4 + 2 + 1 + 2 + 2 + 2 + 2 + 1;
-    static constexpr int oPlan = oBar + kNumBars * 8;              // int64 rem; int b, g, i, t
-    static constexpr int oMisc = oPlan + 32;                       // tmem base, abort flag
+    // pv_done[2], o_free[2], x_full, v_ask, v_fixed, drain[2]
+    static constexpr int kNumBars = 4 * kPfStages + 4 + 2 + 1 + 2 + 2 + 2 + 1 + 2 + 2;
+    static constexpr int kExchange = 2 * kPfRows * 4;              // m, l of the second half's rows
+    static constexpr int oPlan = oBar + kNumBars * 8;              // PfPlan
+    static constexpr int oX = oPlan + 48;
+    static constexpr int oMisc = oX + kExchange;                       // tmem base, abort flag
     static constexpr int kBytes = oMisc + 16;
     static constexpr int kAlloc = kBytes + 1024;
 };
@@ -77,7 +79,7 @@ struct PfParams {
     void *ws;
     int64_t total_q;
     int64_t num_slots;
-    int batch, max_pages, num_pages, num_splits, heads, groups, G, tile_tokens, block_tokens;
+    int batch, max_pages, num_pages, num_splits, heads, groups, G, tile_tokens;
     float scale_log2;
 };
 
@@ -100,8 +102,8 @@ __device__ __forceinline__ PfSeq pf_seq(const PfParams &p, int b) {
     return ragged_seq(p.q_starts, p.seqlens, b, p.total_q, p.max_pages);
 }
 
-__device__ __forceinline__ int64_t pf_seq_tiles(const PfParams &p, const PfSeq &s) {
-    return s.n > 0 ? p.groups * pf_tiles_before(s.n, s.L, p.block_tokens, pf_blocks(s.n, p.block_tokens)) : 0;
+__device__ __forceinline__ int64_t pf_seq_units(const PfParams &p, const PfSeq &s) {
+    return s.n > 0 ? p.groups * pf_units_before(s.n, s.L, p.tile_tokens, pf_blocks(s.n, p.tile_tokens)) : 0;
 }
 
 __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
@@ -120,61 +122,66 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v) {
     return v;
 }
 
-// One full warp: the batch's (block, tile) pairs; sequences with bad numbers are reported
-// when `report`.
-__device__ int64_t pf_total(const PfParams &p, bool report) {
-    int64_t acc = 0;
-    for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
-        const PfSeq s = pf_seq(p, b);
-        if (s.bad && report) report_error(p.ws, GQLA_ERR_DEVICE, b);
-        acc += pf_seq_tiles(p, s);
-    }
-    return warp_sum64(acc);
-}
-
-// A place in the plan: sequence, group, block, tile, and (block_start) the position of the
-// block's first pair.
-struct PfPlace {
+// A pair's chunk: units [start of block (b, g, i), end) from tile t of that block on; `len`
+// is the length of every chunk. Nothing to do if b is past the batch.
+struct PfPlan {
+    int64_t u0, end, len;
     int b, g, i, t;
-    int64_t block_start;
 };
 
-// One full warp: the place of pair `pos` (0 <= pos < total).
-__device__ PfPlace pf_find(const PfParams &p, int64_t pos) {
+// One full warp: the plan of chunk c. Sequences with bad numbers are reported when `report`.
+__device__ PfPlan pf_plan(const PfParams &p, int c, bool report) {
     const int lane = threadIdx.x & 31;
-    PfPlace r{p.batch, 0, 0, 0, 0};
+    PfPlan r{0, 0, 0, p.batch, 0, 0, 0};
+    // the first 32 sequences stay in registers: a small batch is read once
+    PfSeq s0{0, 0, 0, false};
+    int64_t units0 = 0, total = 0;
+    for (int b = lane; b < p.batch; b += 32) {
+        const PfSeq s = pf_seq(p, b);
+        if (s.bad && report) report_error(p.ws, GQLA_ERR_DEVICE, b);
+        const int64_t u = pf_seq_units(p, s);
+        total += u;
+        if (b < 32) { s0 = s; units0 = u; }
+    }
+    total = warp_sum64(total);
+    r.len = pf_chunk(total, p.num_splits);
+    const int64_t pos = c * r.len;
+    if (pos >= total) return r;
+    r.end = min(total, pos + r.len);
     int64_t base = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int b = b0 + lane;
         PfSeq s{0, 0, 0, false};
-        if (b < p.batch) s = pf_seq(p, b);
-        const int64_t mine = pf_seq_tiles(p, s);
+        int64_t mine = 0;
+        if (b0 == 0) { s = s0; mine = units0; }
+        else if (b < p.batch) { s = pf_seq(p, b); mine = pf_seq_units(p, s); }
         const int64_t incl = warp_scan64(mine);
         const unsigned hit = __ballot_sync(0xffffffffu, mine > 0 && base + incl > pos);
         if (hit) {
             const int src = __ffs(hit) - 1;
             const int64_t start = base + __shfl_sync(0xffffffffu, incl - mine, src);
             const int n = __shfl_sync(0xffffffffu, s.n, src), L = __shfl_sync(0xffffffffu, s.L, src);
-            const int W = p.block_tokens, m = pf_blocks(n, W);
-            const int64_t per_group = pf_tiles_before(n, L, W, m);
+            const int T = p.tile_tokens, m = pf_blocks(n, T);
+            const int64_t per_group = __shfl_sync(0xffffffffu, mine, src) / p.groups;
             int64_t off = pos - start;
             r.b = b0 + src;
             r.g = (int)(off / per_group);
             off -= r.g * per_group;
-            // the block whose pairs hold `off`: the last i with tiles_before(i) <= off
-            int lo = 0, hi = m;  // tiles_before(lo) <= off < tiles_before(hi)
+            // the block that holds unit `off`: the last i with units_before(i) <= off
+            int lo = 0, hi = m;
             while (hi - lo > 1) {
                 const int step = (hi - lo + 31) / 32;
-                const int c = lo + (lane + 1) * step;
-                const bool le = c < hi && pf_tiles_before(n, L, W, c) <= off;
+                const int at = lo + (lane + 1) * step;
+                const bool le = at < hi && pf_units_before(n, L, T, at) <= off;
                 const int k = __popc(__ballot_sync(0xffffffffu, le));
                 hi = min(hi, lo + (k + 1) * step);
                 lo += k * step;
             }
             r.i = lo;
-            const int64_t before = pf_tiles_before(n, L, W, lo);
-            r.t = (int)(off - before);
-            r.block_start = pos - r.t;
+            off -= pf_units_before(n, L, T, lo);
+            r.u0 = pos - off;
+            const int w = pf_weight(min(n - lo * 4 * T, 4 * T), T);
+            r.t = (int)((off + w - 1) / w);  // the first tile that starts in the chunk
             return r;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
@@ -196,23 +203,16 @@ struct PfPiece {
 // Walks the pieces of a chunk; the same in every role.
 struct PfIter {
     PfSeq s;
+    int64_t u0, end;  // first unit of the next block, end of the chunk
     int b, g, i, t;
-    int64_t rem;
     bool started;
-    __device__ __forceinline__ PfIter(const PfParams &p, const int *plan) {
-        rem = *reinterpret_cast<const int64_t *>(plan);
-        b = plan[2];
-        g = plan[3];
-        i = plan[4];
-        t = plan[5];
-        started = false;
-        if (rem > 0 && b < p.batch) s = pf_seq(p, b);
+    __device__ __forceinline__ PfIter(const PfParams &p, const PfPlan &plan)
+        : u0(plan.u0), end(plan.end), b(plan.b), g(plan.g), i(plan.i), t(plan.t), started(false) {
+        if (b < p.batch) s = pf_seq(p, b);
     }
     __device__ __forceinline__ bool next(const PfParams &p, PfPiece &o) {
-        if (rem <= 0) return false;
-        if (started) {
-            t = 0;
-            if (++i * p.block_tokens >= s.n) {
+        while (u0 < end) {
+            if (started && (++i * 4 * p.tile_tokens >= s.n)) {
                 i = 0;
                 if (++g == p.groups) {
                     g = 0;
@@ -222,23 +222,37 @@ struct PfIter {
                     } while (b < p.batch && s.n == 0);
                 }
             }
+            started = true;
+            if (b >= p.batch) return false;
+            const int first = i * 4 * p.tile_tokens;
+            o.b = b;
+            o.g = g;
+            o.row0 = s.q0 + first;
+            o.ntok = min(4 * p.tile_tokens, s.n - first);
+            o.pos0 = s.L - s.n + first;
+            o.kv_end = o.pos0 + o.ntok;
+            o.nt = (o.kv_end + kPfTile - 1) / kPfTile;
+            const int w = pf_weight(o.ntok, p.tile_tokens);
+            o.t0 = t;
+            o.t1 = (int)min((int64_t)o.nt, (end - u0 + w - 1) / w);
+            t = 0;
+            u0 += (int64_t)w * o.nt + kPfBlockCost;
+            if (o.t0 < o.t1) return true;
         }
-        started = true;
-        if (b >= p.batch) return false;
-        const int first = i * p.block_tokens;
-        o.b = b;
-        o.g = g;
-        o.row0 = s.q0 + first;
-        o.ntok = min(p.block_tokens, s.n - first);
-        o.pos0 = s.L - s.n + first;
-        o.kv_end = o.pos0 + o.ntok;
-        o.nt = (o.kv_end + kPfTile - 1) / kPfTile;
-        o.t0 = t;
-        o.t1 = (int)min((int64_t)o.nt, t + rem);
-        rem -= o.t1 - o.t0;
-        return true;
+        return false;
     }
 };
+
+// The merge of the block that begins in chunk c and goes on: pieces in `parts` chunks (0: none
+// does), rows of tokens [row0, row0 + ntok), group g. One record per chunk, behind the LSE rows
+// of the partials.
+struct PfMerge {
+    int parts, row0, ntok, g;
+};
+
+__device__ __forceinline__ PfMerge *pf_merge(const PfParams &p, int c) {
+    return reinterpret_cast<PfMerge *>(p.lse_part + (int64_t)2 * p.num_splits * kPfBlockRows) + c;
+}
 
 // TMEM columns: P of the two query tiles (bf16, 64 columns each) with the one S between
 // them, then O. The tiles take turns with S: it is free again as soon as the softmax has
@@ -282,29 +296,11 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     return d;
 }
 
-// 2^x of two values on the FMA pipes: x = n + f with n = round(x), |f| <= 1/2 (Cody-Waite),
-// 2^f by its minimax polynomial of degree 4 (Remez exchange; relative error 2.7e-6, against
-// the 2^-9 of P in bf16), n added to the exponent. For finite x <= 127; below -126 it gives
-// about 2^-126.
-__device__ __forceinline__ float2 exp2_fma(float2 x) {
-    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: x + kMagic holds round(x) in its low bits
-    x.x = fmaxf(x.x, -126.0f);
-    x.y = fmaxf(x.y, -126.0f);
-    const float2 n = add2(x, make_float2(kMagic, kMagic));
-    const float2 f = add2(x, fma2(n, make_float2(-1.0f, -1.0f), make_float2(kMagic, kMagic)));
-    float2 r = make_float2(0.00957010221f, 0.00957010221f);
-    r = fma2(r, f, make_float2(0.0559178591f, 0.0559178591f));
-    r = fma2(r, f, make_float2(0.240247443f, 0.240247443f));
-    r = fma2(r, f, make_float2(0.693121791f, 0.693121791f));
-    r = fma2(r, f, make_float2(0.999999285f, 0.999999285f));
-    return make_float2(__uint_as_float(__float_as_uint(r.x) + (__float_as_uint(n.x) << 23)),
-                       __uint_as_float(__float_as_uint(r.y) + (__float_as_uint(n.y) << 23)));
-}
-
 // P = 2^(s scale - mu) of a row's 128 scores, rounded to bf16, into the row's P columns;
-// returns the sum of the unrounded values. FAST: also the largest score, and every fourth
-// pair of exponentials on the FMA pipes (the 16 a cycle of the special-function unit bound
-// the loop otherwise); scores must be finite or `mx` NaN says that they were not.
+// returns the sum of the unrounded values. FAST: also the largest score (NaN if one is).
+// (A share of the exponentials as polynomials on the FMA pipes does not pay here: the issue
+// slots and the power that they take cost more than the special-function unit's time. Step of
+// 128 keys: 3080 cycles without, 3190 with a quarter, 3610 with half.)
 template <bool FAST, typename Ready>
 __device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, float mu, uint32_t t_p, float &mx,
                                         Ready ready) {
@@ -318,9 +314,7 @@ __device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, 
         for (int e = 0; e < 32; e += 2) {
             const float2 s = make_float2(__uint_as_float(sv[i + e]), __uint_as_float(sv[i + e + 1]));
             const float2 x = fma2(s, sc, sub);
-            float2 v;
-            if (FAST && e % 8 == 6) v = exp2_fma(x);
-            else v = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            const float2 v = make_float2(fast_exp2(x.x), fast_exp2(x.y));
             if (FAST) top[(e >> 1) & 1] = max3_nan(top[(e >> 1) & 1], s.x, s.y);
             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], v);
             __nv_bfloat162 h2 = __floats2bfloat162_rn(v.x, v.y);
@@ -345,8 +339,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     uint64_t *q_full = v_empty + kPfStages, *q_empty = q_full + 2;
     uint64_t *s_full = q_empty + 2, *s_free = s_full + 2, *p_full = s_free + 1, *pv_done = p_full + 2;
     uint64_t *o_free = pv_done + 2;
-    uint64_t *v_ask = o_free + 2, *v_fixed = v_ask + 1, *drain = v_fixed + 1;
-    int *plan = reinterpret_cast<int *>(smem + SM::oPlan);
+    uint64_t *x_full = o_free + 2, *v_ask = x_full + 1, *v_fixed = v_ask + 1, *drain = v_fixed + 1;
+    PfPlan &plan = *reinterpret_cast<PfPlan *>(smem + SM::oPlan);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::oMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::oMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -366,16 +360,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             mbar_init(&pv_done[i], 1); mbar_init(&o_free[i], 8);
         }
         mbar_init(s_free, 8);
+        mbar_init(x_full, 4);
         mbar_init(v_ask, 1);
         mbar_init(v_fixed, 2);
-        mbar_init(drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&kv_map);
         prefetch_tensormap(&kr_map);
         prefetch_tensormap(&q_map);
     }
-    if (warp == 2) {
+    if (warp == 3) {
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
         tc_fence_before();
@@ -383,27 +379,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 0) {
-        const int64_t total = pf_total(p, blockIdx.x == 0);
-        const int64_t k = (total + p.num_splits - 1) / p.num_splits;
-        const int64_t r0 = c * k, rem = min(total, r0 + k) - r0;
-        PfPlace at{0, 0, 0, 0, 0};
-        if (rem > 0) at = pf_find(p, r0);
-        if (lane == 0) {
-            *reinterpret_cast<int64_t *>(plan) = rem > 0 ? rem : 0;
-            plan[2] = at.b; plan[3] = at.g; plan[4] = at.i; plan[5] = at.t;
-        }
+        const PfPlan mine = pf_plan(p, c, blockIdx.x == 0);
+        if (lane == 0) plan = mine;
     }
     __syncthreads();
     cluster_sync();  // the other CTA's barriers are initialised too
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t steps = (uint32_t)*reinterpret_cast<const int64_t *>(plan);
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfIssueRegs));
         if (warp == 0) {
             // ------------------------------------------------------------ TMA producer
-            if (steps > 0 && elect_one()) {
+            if (elect_one()) {
                 uint32_t kn = 0, vn = 0, qn[2] = {0, 0};
                 // the next stage of a ring, once it is free
                 auto stage = [&](uint64_t *fullb, uint64_t *emptyb, uint32_t n, uint32_t bytes) -> int {
@@ -478,97 +466,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     if (qn[q] && !*abort_flag && !mbar_wait(&q_empty[q], (qn[q] - 1) & 1, abort_flag)) *abort_flag = 1;
             }
         } else if (warp == 1) {
-            // ------------------------------------------------------------ MMA issuer
-            if (rank == 0 && steps > 0 && elect_one()) {
-                constexpr uint32_t idesc_s = idesc_bf16(2 * kPfRows, kPfTile, 0, 0);
-                constexpr uint32_t idesc_pv = idesc_bf16(2 * kPfRows, kDv, 0, 1);
-                // descriptor words: q and K K-major, V MN-major, all 128-byte swizzled rows
+            // ------------------------------------------------------------ S issuer
+            // S_q of every step in turn, each as soon as the softmax has read the one before it
+            if (rank == 0 && elect_one()) {
+                constexpr uint32_t idesc = idesc_bf16(2 * kPfRows, kPfTile, 0, 0);
+                // descriptor words: q and K K-major, 128-byte swizzled rows
                 const uint64_t q_d = smem_desc(smem_u32(smem + SM::oQ), 16, 1024, kSw128);
                 const uint32_t hi = static_cast<uint32_t>(q_d >> 32), q_lo = static_cast<uint32_t>(q_d);
-                const uint32_t k_lo0 = static_cast<uint32_t>(smem_desc(smem_u32(smem + SM::oK), 16, 1024, kSw128));
-                const uint32_t v_lo0 = static_cast<uint32_t>(smem_desc(smem_u32(smem + SM::oV), 16, 1024, kSw128));
-                uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0}, fixes = 0, sn = 0;
-                auto wait = [&](uint64_t *bar, uint32_t parity) {
-                    if (!mbar_wait(bar, parity, abort_flag)) *abort_flag = 1;
-                };
-                // S_q of step s; the step's last query tile frees K, a piece's last step the query tile
-                auto score = [&](const PfPiece &pc, int t, uint32_t s, int q, int nq) {
-                    if (t == pc.t0) wait(&q_full[q], qn[q]++ & 1);
-                    const int st = s % kPfStages;
-                    if (q == 0) wait(&k_full[st], (s / kPfStages) & 1);
-                    if (sn++ > 0) wait(s_free, sn & 1);  // the softmax has read the S before this one
-                    tc_fence_after();
-                    const uint32_t a = q_lo + q * (3 * kPfQBlock >> 4), b = k_lo0 + st * (kPfK >> 4);
+                const uint32_t k_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + SM::oK), 16, 1024, kSw128));
+                uint32_t qn[2] = {0, 0}, sn = 0, s = 0;
+                PfIter it(p, plan);
+                PfPiece pc;
+                while (!*abort_flag && it.next(p, pc)) {
+                    const int nq = pc.ntok > 2 * p.tile_tokens ? 2 : 1;
+                    for (int t = pc.t0; t < pc.t1 && !*abort_flag; ++t, ++s) {
+                        const int st = s % kPfStages;
 #pragma unroll
-                    for (int ks = 0; ks < 12; ++ks)
-                        mma_bf16_pair(tmem + kPfColS, a + ((ks >> 2) * kPfQBlock + (ks & 3) * 32 >> 4),
-                                      b + ((ks >> 2) * kPfBox + (ks & 3) * 32 >> 4), hi, idesc_s, ks > 0 ? 1u : 0u);
-                    mma_commit_pair(&s_full[q]);
-                    if (q == nq - 1) mma_commit_pair(&k_empty[st]);
-                    if (t == pc.t1 - 1) mma_commit_pair(&q_empty[q]);
-                };
-                // O_q of step s
-                auto product = [&](const PfPiece &pc, int t, uint32_t s, int q, int nq) {
-                    const int st = s % kPfStages;
-                    if (q == 0) {
-                        wait(&v_full[st], (s / kPfStages) & 1);
-                        if (t == pc.nt - 1 && pc.kv_end % kPfTile != 0) {
-                            mbar_arrive_remote(map_peer(smem_u32(v_ask), 0));
-                            mbar_arrive_remote(map_peer(smem_u32(v_ask), 1));
-                            if (!mbar_wait_cluster(v_fixed, fixes++ & 1, abort_flag)) *abort_flag = 1;
+                        for (int q = 0; q < 2; ++q) {
+                            if (nq == 1 && q != ((t - pc.t0) & 1)) continue;
+                            const int qt = nq == 2 ? q : 0;  // query tile
+                            bool ok = true;
+                            if (t == pc.t0) ok = mbar_wait(&q_full[qt], qn[qt]++ & 1, abort_flag);
+                            if (qt == 0) ok = ok && mbar_wait(&k_full[st], (s / kPfStages) & 1, abort_flag);
+                            if (sn++ > 0) ok = ok && mbar_wait(s_free, sn & 1, abort_flag);
+                            if (!ok) *abort_flag = 1;
+                            tc_fence_after();
+                            const uint32_t a = q_lo + qt * (3 * kPfQBlock >> 4), b = k_lo + st * (kPfK >> 4);
+#pragma unroll
+                            for (int ks = 0; ks < 12; ++ks)
+                                mma_bf16_pair(tmem + kPfColS, a + ((ks >> 2) * kPfQBlock + (ks & 3) * 32 >> 4),
+                                              b + ((ks >> 2) * kPfBox + (ks & 3) * 32 >> 4), hi, idesc, ks > 0 ? 1u : 0u);
+                            mma_commit_pair(&s_full[q]);
+                            if (qt == nq - 1) mma_commit_pair(&k_empty[st]);  // the step's last query tile
+                            if (t == pc.t1 - 1) mma_commit_pair(&q_empty[qt]);
                         }
                     }
-                    if (t == pc.t0) wait(&o_free[q], (on[q]++ & 1) ^ 1);
-                    wait(&p_full[q], pn[q]++ & 1);
-                    tc_fence_after();
-                    const uint32_t b = v_lo0 + st * (kPfV >> 4);
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_bf16_ts_pair(tmem + o_col(q), tmem + p_col(q) + 8 * ks, b + (ks * 2048 >> 4), hi, idesc_pv,
-                                         (ks > 0 || t > pc.t0) ? 1u : 0u);
-                    mma_commit_pair(&pv_done[q]);
-                    if (q == nq - 1) mma_commit_pair(&v_empty[st]);
-                };
-                PfIter it(p, plan);
-                PfPiece pc, nx;
-                it.next(p, pc);
-                int t = pc.t0, nq = pc.ntok > 2 * p.tile_tokens ? 2 : 1;
-                for (int q = 0; q < nq; ++q) score(pc, t, 0, q, nq);
-                for (uint32_t s = 0; s < steps && !*abort_flag; ++s) {
-                    // the step after this one
-                    nx = pc;
-                    int nt = t + 1, nnq = nq;
-                    bool more = true;
-                    if (nt == pc.t1) {
-                        more = it.next(p, nx);
-                        nt = nx.t0;
-                        nnq = nx.ntok > 2 * p.tile_tokens ? 2 : 1;
-                    }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        if (more && q < nnq) score(nx, nt, s + 1, q, nnq);
-                        if (q < nq) product(pc, t, s, q, nq);
-                    }
-                    pc = nx;
-                    t = nt;
-                    nq = nnq;
                 }
                 // nothing may still be running when TMEM is freed
-                mma_commit_pair(drain, 1);
+                mma_commit_pair(&drain[0], 1);
                 int dummy = 0;
-                mbar_wait(drain, 0, reinterpret_cast<volatile int *>(&dummy));
+                mbar_wait(&drain[0], 0, reinterpret_cast<volatile int *>(&dummy));
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ O issuer
+            // O_q += P_q V of every step in turn
+            if (rank == 0 && elect_one()) {
+                constexpr uint32_t idesc = idesc_bf16(2 * kPfRows, kDv, 0, 1);
+                const uint64_t v_d = smem_desc(smem_u32(smem + SM::oV), 16, 1024, kSw128);  // V MN-major
+                const uint32_t hi = static_cast<uint32_t>(v_d >> 32), v_lo = static_cast<uint32_t>(v_d);
+                uint32_t pn[2] = {0, 0}, on[2] = {0, 0}, fixes = 0, s = 0;
+                PfIter it(p, plan);
+                PfPiece pc;
+                while (!*abort_flag && it.next(p, pc)) {
+                    const int nq = pc.ntok > 2 * p.tile_tokens ? 2 : 1;
+                    for (int t = pc.t0; t < pc.t1 && !*abort_flag; ++t, ++s) {
+                        const int st = s % kPfStages;
+                        const uint32_t b = v_lo + st * (kPfV >> 4);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            if (nq == 1 && q != ((t - pc.t0) & 1)) continue;
+                            const bool fresh = t - pc.t0 == (nq == 1 ? q : 0);  // O_q starts here
+                            bool ok = true;
+                            if (nq == 1 || q == 0) {
+                                ok = mbar_wait(&v_full[st], (s / kPfStages) & 1, abort_flag);
+                                if (t == pc.nt - 1 && pc.kv_end % kPfTile != 0) {
+                                    mbar_arrive_remote(map_peer(smem_u32(v_ask), 0));
+                                    mbar_arrive_remote(map_peer(smem_u32(v_ask), 1));
+                                    ok = ok && mbar_wait_cluster(v_fixed, fixes++ & 1, abort_flag);
+                                }
+                            }
+                            if (fresh) ok = ok && mbar_wait(&o_free[q], (on[q]++ & 1) ^ 1, abort_flag);
+                            ok = ok && mbar_wait(&p_full[q], pn[q]++ & 1, abort_flag);
+                            if (!ok) *abort_flag = 1;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks)
+                                mma_bf16_ts_pair(tmem + o_col(q), tmem + p_col(q) + 8 * ks, b + (ks * 2048 >> 4), hi, idesc,
+                                                 (ks > 0 || !fresh) ? 1u : 0u);
+                            mma_commit_pair(&pv_done[q]);
+                            if (nq == 1 || q == 1) mma_commit_pair(&v_empty[st]);
+                        }
+                    }
+                }
+                mma_commit_pair(&drain[1], 1);
+                int dummy = 0;
+                mbar_wait(&drain[1], 0, reinterpret_cast<volatile int *>(&dummy));
             }
         } else if (warp == 3) {
             // ------------------------------------------------------------ V rows past the keys
             // The last tile of a block ends at its last query token, rarely at the tile's end:
             // the rows past it (later tokens, or slots that hold no token and may hold NaN) meet
             // P = 0 in the product and are cleared so that 0 x NaN cannot enter it.
-            // The MMA issuer asks for it once V has landed and waits until it is done.
+            // The O issuer asks for it once V has landed and waits until it is done.
             PfIter it(p, plan);
             PfPiece pc;
+            PfMerge merge{0, 0, 0, 0};
             uint32_t s = 0, fixes = 0;
             while (it.next(p, pc)) {
                 s += pc.t1 - pc.t0;
+                if (pc.t0 == 0 && pc.t1 < pc.nt) {  // begins here, goes on: where does its last tile lie
+                    const int64_t tail = kPfBlockCost + pf_weight(pc.ntok, p.tile_tokens);
+                    merge = PfMerge{(int)((it.u0 - tail) / plan.len) - c + 1, (int)pc.row0, pc.ntok, pc.g};
+                }
                 const int keep = pc.kv_end % kPfTile;
                 if (pc.t1 != pc.nt || keep == 0) continue;
                 if (!__all_sync(0xffffffffu, mbar_wait_long<true>(v_ask, fixes++ & 1, abort_flag))) break;
@@ -582,8 +581,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(lead(v_fixed));
             }
+            if (p.num_splits > 1 && rank == 0 && lane == 0) *pf_merge(p, c) = merge;
         }
-        // warp 2 owns TMEM and is otherwise idle
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfSoftmaxRegs));
         // ---------------------------------------------------------------- softmax, epilogue
@@ -591,7 +590,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         const int row = 32 * (warp & 3) + lane;    // this thread's query row: its TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t t_s = tmem + kPfColS + lane_off, t_p = tmem + p_col(q) + lane_off, t_o = tmem + o_col(q) + lane_off;
-        const int tok = (2 * q + (int)rank) * p.tile_tokens + row / p.G, hg = row % p.G;  // token of the block, head of the group
+        const int hg = row % p.G;                  // head of the group
+        float *const xm = reinterpret_cast<float *>(smem + SM::oX), *const xl = xm + kPfRows;
+        uint32_t xn = 0;
         const bool in_tile = row < p.tile_tokens * p.G;
         uint32_t sn = 0, pvn = 0;  // steps seen, and products of this tile known to be complete
         PfIter it(p, plan);
@@ -606,12 +607,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             }
         };
         while (alive && it.next(p, pc)) {
-            if (2 * q * p.tile_tokens >= pc.ntok) continue;
+            // a block of one MMA tile: both warpgroups take its rows, the even and the odd key
+            // tiles, and the first joins the two at the end
+            const bool one = pc.ntok <= 2 * p.tile_tokens, joined = one && pc.t1 - pc.t0 > 1;
+            if (one && q == 1 && !joined) continue;
+            const int part = (one ? 0 : 2 * q) + (int)rank;        // 128-row part of the block
+            const int tok = part * p.tile_tokens + row / p.G;      // token of the block
             const bool valid = in_tile && tok < pc.ntok;
             const bool warp_valid = __any_sync(0xffffffffu, valid);
             const int last = pc.pos0 + tok;   // the last key this row sees
             float m = -INFINITY, l = 0.0f;    // maximum (log2 units) and sum of this row
-            for (int t = pc.t0; t < pc.t1; ++t) {
+            const int t_first = pc.t0 + (one ? q : 0);
+            for (int t = t_first; t < pc.t1; t += one ? 2 : 1) {
                 alive = __all_sync(0xffffffffu, mbar_wait_long<false>(&s_full[q], sn++ & 1, abort_flag)) && alive;
                 if (!alive) break;
                 tc_fence_after();
@@ -629,7 +636,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     // than 2^8 above it (and on a piece's first tile, and under a mask) again
                     // against the new one. A NaN score takes the second way.
                     float lt = 0.0f;
-                    bool redo = t == pc.t0 || masked;
+                    bool redo = t == t_first || masked;
                     if (!redo) {
                         float mx;
                         lt = form_p<true>(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_p, mx, [&] { products(sn - 1); });
@@ -651,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                         if (rise) m = mt;
                         l *= a;
                         products(sn - 1);
-                        if (t > pc.t0 && __any_sync(0xffffffffu, rise)) {
+                        if (t > t_first && __any_sync(0xffffffffu, rise)) {
 #pragma unroll 1
                             for (int i = 0; i < kDv; i += 16) {
                                 uint32_t r[16];
@@ -681,44 +688,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             if (alive) products(sn - 1);
             if (alive) products(sn);
             if (!alive) break;
+            if (joined && q == 1) {  // this half's O stays in TMEM, where the same lanes read it
+                xm[row] = m;
+                xl[row] = l;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x_full);
+                continue;
+            }
+            float a0 = 1.0f, a1 = 0.0f;
+            if (joined) {
+                alive = __all_sync(0xffffffffu, mbar_wait(x_full, xn++ & 1, abort_flag));
+                if (!alive) break;
+                tc_fence_after();
+                const float m1 = xm[row], top = fmaxf(m, m1);
+                a0 = m == -INFINITY ? 0.0f : fast_exp2(m - top);
+                a1 = m1 == -INFINITY ? 0.0f : fast_exp2(m1 - top);
+                l = l * a0 + xl[row] * a1;
+                m = top;
+            }
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             const float lse = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            const float w0 = a0 * inv, w1 = a1 * inv;
             const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
-            const int64_t prow = (int64_t)(2 * c + (pc.t0 == 0 ? 1 : 0)) * kPfBlockRows + (2 * q + (int)rank) * kPfRows + row;
+            const int64_t prow = (int64_t)(2 * c + (pc.t0 == 0 ? 1 : 0)) * kPfBlockRows + part * kPfRows + row;
             const int64_t orow = (pc.row0 + tok) * p.heads + pc.g * p.G + hg;
             if (warp_valid) {
                 if (valid) {
                     if (!whole) p.lse_part[prow] = lse;
                     else if (p.lse_out) p.lse_out[orow] = lse;
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < kDv; i += 32) {
                     uint32_t r[32];
                     tmem_ld32(t_o + i, r);
                     tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * w0);
+                    if (joined) {
+                        uint32_t r1[32];
+                        tmem_ld32(t_o + kDv + i, r1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            r[e] = __float_as_uint(fmaf(__uint_as_float(r1[e]), w1, __uint_as_float(r[e])));
+                    }
                     if (!valid) continue;
                     if (whole) {
                         uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * kDv + i);
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
-                            const uint2 a = pack_bf16x4(__uint_as_float(r[e]) * inv, __uint_as_float(r[e + 1]) * inv,
-                                                        __uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
-                            const uint2 b = pack_bf16x4(__uint_as_float(r[e + 4]) * inv, __uint_as_float(r[e + 5]) * inv,
-                                                        __uint_as_float(r[e + 6]) * inv, __uint_as_float(r[e + 7]) * inv);
+                            const uint2 a = pack_bf16x4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]),
+                                                        __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+                            const uint2 b = pack_bf16x4(__uint_as_float(r[e + 4]), __uint_as_float(r[e + 5]),
+                                                        __uint_as_float(r[e + 6]), __uint_as_float(r[e + 7]));
                             dst[e / 8] = make_uint4(a.x, a.y, b.x, b.y);
                         }
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.o_part + prow * kDv + i);
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + prow * kDv + i);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            dst[e / 4] = make_float4(__uint_as_float(r[e]) * inv, __uint_as_float(r[e + 1]) * inv,
-                                                     __uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
+                        for (int e = 0; e < 32; e += 4) dst[e / 4] = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote_relaxed(lead(&o_free[q]));
+            if (lane == 0) {
+                mbar_arrive_remote_relaxed(lead(&o_free[q]));
+                if (joined) mbar_arrive_remote_relaxed(lead(&o_free[1]));
+            }
         }
         if (!alive) *abort_flag = 1;
     }
@@ -738,57 +776,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         while (clock64() - t0 < 200000) {}
     }
     cluster_sync();
-    if (warp == 2) {
+    if (warp == 3) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Merge of the cut blocks. CTA (c - 1, y) looks at the boundary between the chunks c - 1
-// and c: if it is the first one inside its block (the block begins in chunk c - 1), the
-// CTA merges the block's pieces, slots 2 (c - 1) + 1, 2 c, 2 (c + 1), ... up to the chunk
-// that holds its last pair, for the rows 32 y .. 32 y + 31. One warp per row, four columns
-// a lane, partials in chunk order.
+// Merge of the divided blocks: CTA (c, y) the rows 32 y .. 32 y + 31 of the block that begins
+// in chunk c, if it goes on: slots 2 c + 1, 2 (c + 1), 2 (c + 2), ... One warp per row, four
+// columns a lane, partials in chunk order.
 // ---------------------------------------------------------------------------
 constexpr int kPcRows = 32, kPcWarps = 8;
 
 __global__ void __launch_bounds__(32 * kPcWarps) prefill_combine_kernel(const PfParams p) {
-    __shared__ int64_t s_end;
-    __shared__ int s_b, s_g, s_i, s_go;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x + 1;
+    const int c = blockIdx.x;
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 0) {
-        const int64_t total = pf_total(p, false);
-        const int64_t k = (total + p.num_splits - 1) / p.num_splits;
-        const int64_t at = c * k;
-        int go = 0;
-        if (k > 0 && at < total) {
-            const PfPlace w = pf_find(p, at);
-            go = w.t > 0 && w.block_start >= at - k;
-            if (go && lane == 0) {
-                const PfSeq s = pf_seq(p, w.b);
-                const int last = min((w.i + 1) * p.block_tokens, s.n);
-                s_end = (w.block_start + (s.L - s.n + last + kPfTile - 1) / kPfTile - 1) / k;  // chunk of its last pair
-                s_b = w.b; s_g = w.g; s_i = w.i;
-            }
-        }
-        if (lane == 0) s_go = go;
-    }
-    __syncthreads();
-    if (!s_go) return;
-    const PfSeq s = pf_seq(p, s_b);
-    const int first = s_i * p.block_tokens;
-    const int parts = (int)(s_end - (c - 1)) + 1;
+    const PfMerge mg = *pf_merge(p, c);
+    const int parts = mg.parts;
+    if (parts == 0) return;
     for (int r = blockIdx.y * kPcRows + warp; r < (int)(blockIdx.y + 1) * kPcRows; r += kPcWarps) {
         const int in_tile = r % kPfRows;
         const int tok = r / kPfRows * p.tile_tokens + in_tile / p.G;
-        if (in_tile >= p.tile_tokens * p.G || first + tok >= s.n) continue;
-        // piece x of the block: slot 2 (c - 1) + 1 for the first, 2 (c - 1 + x) after it
+        if (in_tile >= p.tile_tokens * p.G || tok >= mg.ntok) continue;
+        // piece x of the block
         auto slot = [&](int x) -> int64_t {
-            return (int64_t)(2 * (c - 1 + x) + (x == 0 ? 1 : 0)) * kPfBlockRows + r;
+            return (int64_t)(2 * (c + x) + (x == 0 ? 1 : 0)) * kPfBlockRows + r;
         };
         float M = -INFINITY;
         for (int x = lane; x < parts; x += 32) M = fmaxf(M, p.lse_part[slot(x)]);
@@ -809,7 +824,7 @@ __global__ void __launch_bounds__(32 * kPcWarps) prefill_combine_kernel(const Pf
             acc.w = fmaf(w, v.w, acc.w);
         }
         const float inv = den > 0.0f ? 1.0f / den : 0.0f;
-        const int64_t orow = (s.q0 + first + tok) * p.heads + s_g * p.G + in_tile % p.G;
+        const int64_t orow = (int64_t)(mg.row0 + tok) * p.heads + mg.g * p.G + in_tile % p.G;
         *reinterpret_cast<uint2 *>(p.out + orow * kDv + 4 * lane) =
             pack_bf16x4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if (lane == 0 && p.lse_out) p.lse_out[orow] = den > 0.0f ? M + logf(den) : -INFINITY;
@@ -842,7 +857,6 @@ cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_
     p.groups = num_groups;
     p.G = G;
     p.tile_tokens = pf_tile_tokens(G);
-    p.block_tokens = pf_block_tokens(G);
     p.scale_log2 = scale * kLog2e;
     CUtensorMap kvm, krm, qm;
     {

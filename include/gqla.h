@@ -312,10 +312,10 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
  *   kv_expanded, k_rope, num_slots, kv   the expanded cache, as for gqla_decode_gqa;
  *                kv->seqlens counts the new tokens
  *   num_splits   C >= 1: the batch's (query block, group, key tile) triples are cut
- *                into C equal chunks, one per CTA pair (gqla_plan_prefill picks C)
+ *                into C chunks of equal cost, one per CTA pair (gqla_plan_prefill picks C)
  *   o_part       fp32 [gqla_prefill_slots(C)][512][128], lse_part fp32
  *                [gqla_prefill_slots(C)][512]: partials of the query blocks that a cut
- *                divides; may be NULL when C == 1
+ *                divides; 16-byte aligned; may be NULL when C == 1
  *   out          bf16 [total_q][h][128];  lse_out fp32 [total_q][h] or NULL (natural
  *                log, as from gqla_combine).  Rows that belong to no sequence are left
  *                as they were.
@@ -333,7 +333,8 @@ int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, cons
                      int num_splits, float *o_part, float *lse_part, void *out, float *lse_out,
                      void *workspace, size_t workspace_bytes, gqla_stream_t stream);
 
-/* Partial slots (512 rows each) that gqla_prefill_gqa addresses: 2 * num_splits. */
+/* Partial slots (512 rows each) that gqla_prefill_gqa addresses: 2 * num_splits and, for the
+ * records of the merge, one more per 128 splits. */
 int gqla_prefill_slots(int num_splits);
 
 /* Host-side choice of gqla_prefill_gqa's num_splits for known lengths.
