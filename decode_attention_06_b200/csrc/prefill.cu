@@ -57,8 +57,8 @@ struct PfSmem {
     static constexpr int oV = oK + kPfStages * kPfK;               // [stages]
     static constexpr int oBar = oV + kPfStages * kPfV;
     // k_full/k_empty, v_full/v_empty[stages], q_full/q_empty[2], s_full[2], s_free, p_full[2],
-    // pv_done[2], o_free[2], x_full, v_ask, v_fixed, drain[2]
-    static constexpr int kNumBars = 4 * kPfStages + 4 + 2 + 1 + 2 + 2 + 2 + 1 + 2 + 2;
+    // pv_done[2], o_free[2], x_full, v_part[stages], drain[2]
+    static constexpr int kNumBars = 5 * kPfStages + 4 + 2 + 1 + 2 + 2 + 2 + 1 + 2;
     static constexpr int kExchange = 2 * kPfRows * 4;              // m, l of the second half's rows
     static constexpr int oPlan = oBar + kNumBars * 8;              // PfPlan
     static constexpr int oX = oPlan + 48;
@@ -86,11 +86,10 @@ struct PfParams {
 // Bounded wait of a role that may have nothing to do for whole blocks (a query tile that
 // short blocks leave empty, the V rows of blocks that end on a tile): the roles that feed it
 // give up after kWaitCycles and raise the abort flag; its own limit is 32 times that.
-template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity, volatile int *abort) {
     const long long t0 = clock64();
     while (true) {
-        if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
         if (clock64() - t0 > 32 * kWaitCycles) return false;
     }
@@ -328,6 +327,25 @@ __device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, 
     return t.x + t.y;
 }
 
+// Four 16-byte units of each of four neighbouring lanes, transposed: lane j of the four ends
+// with unit j of lane k in its place k.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[16], int lane) {
+#pragma unroll
+    for (int b = 1; b <= 2; b <<= 1) {
+        const bool up = (lane & b) != 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (u & b) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[4 * u + e] : w[4 * (u | b) + e], b);
+                if (up) w[4 * u + e] = got;
+                else w[4 * (u | b) + e] = got;
+            }
+        }
+    }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     prefill_gqa_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap kr_map,
                        const __grid_constant__ CUtensorMap q_map, const PfParams p) {
@@ -339,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     uint64_t *q_full = v_empty + kPfStages, *q_empty = q_full + 2;
     uint64_t *s_full = q_empty + 2, *s_free = s_full + 2, *p_full = s_free + 1, *pv_done = p_full + 2;
     uint64_t *o_free = pv_done + 2;
-    uint64_t *x_full = o_free + 2, *v_ask = x_full + 1, *v_fixed = v_ask + 1, *drain = v_fixed + 1;
+    uint64_t *x_full = o_free + 2, *v_part = x_full + 1, *drain = v_part + kPfStages;
     PfPlan &plan = *reinterpret_cast<PfPlan *>(smem + SM::oPlan);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::oMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::oMisc + 4);
@@ -353,6 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         for (int i = 0; i < kPfStages; ++i) {
             mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1);
+            mbar_init(&v_part[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
@@ -361,8 +380,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         }
         mbar_init(s_free, 8);
         mbar_init(x_full, 4);
-        mbar_init(v_ask, 1);
-        mbar_init(v_fixed, 2);
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
         *abort_flag = 0;
@@ -414,11 +431,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                                  ok1 && pg + 1 < pages ? a1 * kPage : (int)p.num_slots};
                 };
                 // V: both pages, this CTA's 64 columns
-                auto load_v = [&](int g, const Slots &sl) {
+                // (`last`: with rows past the block's keys, through warp 3)
+                auto load_v = [&](int g, const Slots &sl, bool last) {
                     const int st = stage(v_full, v_empty, vn, kPfV);
                     if (st < 0) return;
                     uint8_t *dst = smem + SM::oV + st * kPfV;
-                    const uint32_t bar = lead(&v_full[st]);
+                    if (last) mbar_arrive_expect_tx(&v_part[st], kPfV);
+                    const uint32_t bar = last ? map_peer(smem_u32(&v_part[st]), rank) : lead(&v_full[st]);
                     tma_load_3d_pair(dst, &kv_map, bar, kNope + 64 * (int)rank, sl.s0, g);
                     tma_load_3d_pair(dst + kPfBox, &kv_map, bar, kNope + 64 * (int)rank, sl.s1, g);
                     ++vn;
@@ -427,6 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 PfPiece pc;
                 Slots prev{0, 0};
                 int prev_g = -1;
+                bool prev_last = false;
                 const uint32_t q_bytes = (uint32_t)(p.tile_tokens * p.G) * 128u;
                 while (!*abort_flag && it.next(p, pc)) {
                     for (int q = 0; q < 2 && 2 * q * p.tile_tokens < pc.ntok; ++q) {
@@ -449,12 +469,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                         tma_load_3d_pair(dst + kPfBox, &kv_map, bar, 64, y, pc.g);
                         tma_load_2d_pair(dst + 2 * kPfBox, &kr_map, bar, 0, y);
                         ++kn;
-                        if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev);
+                        if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev, prev_last);
                         prev = sl;
                         prev_g = pc.g;
+                        prev_last = t == pc.nt - 1 && pc.kv_end % kPfTile != 0;
                     }
                 }
-                if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev);
+                if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev, prev_last);
                 // every copy has been used, and the other CTA's commits have arrived here
                 auto drained = [&](uint64_t *emptyb, uint32_t n) {
                     for (uint32_t x = (n > kPfStages ? n - kPfStages : 0); x < n && !*abort_flag; ++x)
@@ -514,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 constexpr uint32_t idesc = idesc_bf16(2 * kPfRows, kDv, 0, 1);
                 const uint64_t v_d = smem_desc(smem_u32(smem + SM::oV), 16, 1024, kSw128);  // V MN-major
                 const uint32_t hi = static_cast<uint32_t>(v_d >> 32), v_lo = static_cast<uint32_t>(v_d);
-                uint32_t pn[2] = {0, 0}, on[2] = {0, 0}, fixes = 0, s = 0;
+                uint32_t pn[2] = {0, 0}, on[2] = {0, 0}, s = 0;
                 PfIter it(p, plan);
                 PfPiece pc;
                 while (!*abort_flag && it.next(p, pc)) {
@@ -527,14 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                             if (nq == 1 && q != ((t - pc.t0) & 1)) continue;
                             const bool fresh = t - pc.t0 == (nq == 1 ? q : 0);  // O_q starts here
                             bool ok = true;
-                            if (nq == 1 || q == 0) {
-                                ok = mbar_wait(&v_full[st], (s / kPfStages) & 1, abort_flag);
-                                if (t == pc.nt - 1 && pc.kv_end % kPfTile != 0) {
-                                    mbar_arrive_remote(map_peer(smem_u32(v_ask), 0));
-                                    mbar_arrive_remote(map_peer(smem_u32(v_ask), 1));
-                                    ok = ok && mbar_wait_cluster(v_fixed, fixes++ & 1, abort_flag);
-                                }
-                            }
+                            if (nq == 1 || q == 0) ok = mbar_wait(&v_full[st], (s / kPfStages) & 1, abort_flag);
                             if (fresh) ok = ok && mbar_wait(&o_free[q], (on[q]++ & 1) ^ 1, abort_flag);
                             ok = ok && mbar_wait(&p_full[q], pn[q]++ & 1, abort_flag);
                             if (!ok) *abort_flag = 1;
@@ -556,8 +570,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             // ------------------------------------------------------------ V rows past the keys
             // The last tile of a block ends at its last query token, rarely at the tile's end:
             // the rows past it (later tokens, or slots that hold no token and may hold NaN) meet
-            // P = 0 in the product and are cleared so that 0 x NaN cannot enter it.
-            // The O issuer asks for it once V has landed and waits until it is done.
+            // P = 0 in the product and are cleared so that 0 x NaN cannot enter it. V of such a
+            // tile arrives on a barrier of this CTA, and this warp passes its bytes on to the
+            // barrier that the O issuer waits for.
             PfIter it(p, plan);
             PfPiece pc;
             PfMerge merge{0, 0, 0, 0};
@@ -570,16 +585,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 }
                 const int keep = pc.kv_end % kPfTile;
                 if (pc.t1 != pc.nt || keep == 0) continue;
-                if (!__all_sync(0xffffffffu, mbar_wait_long<true>(v_ask, fixes++ & 1, abort_flag))) break;
+                const int st = (s - 1) % kPfStages;
+                if (!__all_sync(0xffffffffu, mbar_wait_long(&v_part[st], fixes >> st & 1, abort_flag))) break;
+                fixes ^= 1u << st;
                 for (int h = 0; h < 2; ++h) {
-                    uint8_t *v = smem + SM::oV + (s - 1) % kPfStages * kPfV + h * kPfBox;
+                    uint8_t *v = smem + SM::oV + st * kPfV + h * kPfBox;
                     const int r0 = min(max(keep - kPage * h, 0), kPage);  // first row to clear in this page
                     for (int i = lane; i < (kPage - r0) * 8; i += 32)
                         *reinterpret_cast<uint4 *>(v + r0 * 128 + i * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(lead(v_fixed));
+                if (lane == 0) {
+                    __threadfence_block();
+                    mbar_complete_tx_remote(lead(&v_full[st]), kPfV);
+                }
             }
             if (p.num_splits > 1 && rank == 0 && lane == 0) *pf_merge(p, c) = merge;
         }
@@ -619,7 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             float m = -INFINITY, l = 0.0f;    // maximum (log2 units) and sum of this row
             const int t_first = pc.t0 + (one ? q : 0);
             for (int t = t_first; t < pc.t1; t += one ? 2 : 1) {
-                alive = __all_sync(0xffffffffu, mbar_wait_long<false>(&s_full[q], sn++ & 1, abort_flag)) && alive;
+                alive = __all_sync(0xffffffffu, mbar_wait_long(&s_full[q], sn++ & 1, abort_flag)) && alive;
                 if (!alive) break;
                 tc_fence_after();
                 if (warp_valid) {
@@ -718,6 +738,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     if (!whole) p.lse_part[prow] = lse;
                     else if (p.lse_out) p.lse_out[orow] = lse;
                 }
+                // A lane's row goes out in 64-byte pieces: four lanes trade 16-byte units, so that
+                // they write one piece of one row together (alone, a lane's row would touch a line
+                // of its own with every store of the warp).
+                char *const mine = whole ? reinterpret_cast<char *>(p.out + orow * kDv)
+                                         : reinterpret_cast<char *>(p.o_part + prow * kDv);
+                char *dst[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(valid ? mine : nullptr),
+                                                   (lane & ~3) + k);
+                    dst[k] = a ? reinterpret_cast<char *>(a) + (lane & 3) * 16 : nullptr;
+                }
+                auto store = [&](uint32_t (&w)[16], int at) {
+                    quad_transpose(w, lane);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (dst[k])
+                            *reinterpret_cast<uint4 *>(dst[k] + at) =
+                                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                };
 #pragma unroll 1
                 for (int i = 0; i < kDv; i += 32) {
                     uint32_t r[32];
@@ -733,21 +773,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                         for (int e = 0; e < 32; ++e)
                             r[e] = __float_as_uint(fmaf(__uint_as_float(r1[e]), w1, __uint_as_float(r[e])));
                     }
-                    if (!valid) continue;
+                    uint32_t w[16];
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * kDv + i);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            const uint2 a = pack_bf16x4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]),
-                                                        __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
-                            const uint2 b = pack_bf16x4(__uint_as_float(r[e + 4]), __uint_as_float(r[e + 5]),
-                                                        __uint_as_float(r[e + 6]), __uint_as_float(r[e + 7]));
-                            dst[e / 8] = make_uint4(a.x, a.y, b.x, b.y);
+                        for (int e = 0; e < 16; ++e) {
+                            __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+                            w[e] = *reinterpret_cast<uint32_t *>(&h2);
                         }
+                        store(w, i * 2);
                     } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + prow * kDv + i);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) dst[e / 4] = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+                        for (int h = 0; h < 32; h += 16) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) w[e] = r[h + e];
+                            store(w, (i + h) * 4);
+                        }
                     }
                 }
             }

@@ -565,6 +565,13 @@ __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr
                  : "memory");
 }
 
+// Complete `bytes` of the transaction count of an mbarrier of any CTA of the cluster, as a
+// copy that has landed does.
+__device__ __forceinline__ void mbar_complete_tx_remote(uint32_t cluster_addr, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(cluster_addr), "r"(bytes)
+                 : "memory");
+}
+
 // All threads of all CTAs of the cluster (aligned: every thread executes it).
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
