@@ -650,7 +650,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_relaxed(lead(s_free));
-                    const int lim = valid ? last + 1 - t * kPfTile : 0;  // keys of this tile that the row sees
+                    // keys of this tile that the row sees (rows of no token: whatever; they are
+                    // computed along and never stored)
+                    const int lim = valid ? last + 1 - t * kPfTile : kPfTile;
                     const bool masked = __any_sync(0xffffffffu, lim < kPfTile);
                     // P against the maximum so far, at once; only where a row's score rose more
                     // than 2^8 above it (and on a piece's first tile, and under a mask) again
@@ -660,7 +662,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     if (!redo) {
                         float mx;
                         lt = form_p<true>(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_p, mx, [&] { products(sn - 1); });
-                        redo = __any_sync(0xffffffffu, !(mx * p.scale_log2 <= m + kPfRescaleLog2));
+                        redo = __any_sync(0xffffffffu, valid && !(mx * p.scale_log2 <= m + kPfRescaleLog2));
                     }
                     if (redo) {
                         if (masked) {

@@ -24,7 +24,9 @@ namespace gqla {
 constexpr int kPfTile = 128;        // keys per tile (two pages)
 constexpr int kPfRows = 128;        // query rows of one CTA in an MMA tile
 constexpr int kPfBlockRows = 512;   // query rows of a block: two MMA tiles over two CTAs
-constexpr int kPfBlockCost = 2;     // units for a block's start and end
+// Units for a block's start and end: a step of two MMA tiles (2 units) takes 3500 cycles, a
+// block 8000 more (fitted to the spread of the pairs' times over prompts of 130 to 8192 tokens).
+constexpr int kPfBlockCost = 5;
 
 // Query tokens of a CTA's part of an MMA tile, for G heads per group: T.
 __host__ __device__ inline int pf_tile_tokens(int G) { return kPfRows / G; }
