@@ -3,15 +3,15 @@
 // shared RoPE key (GQLA, paperlayer.ai summary, sec. 3 "Two equivalent decoding paths": what
 // the one-shot expansion does to a whole cache, done to the tokens of one step or prompt).
 //
-//   D[128 rows x NC] = A[128 x 512] * B[512 x NC],  NC = 256: B = [W_UK_g | W_UV_g], or
-//   NC = 128: one of the two
+//   D[256 rows x 256] = A[256 x 512] * B_g[512 x 256],  B_g = [W_UK_g | W_UV_g]
 //
-// A CTA takes 128 rows (A, K-major, 128 KB, stays in shared memory) and a share of the
-// groups; B streams through a ring of 32-row slabs (MN-major, the weights as stored); two
-// TMEM accumulators let the epilogue of one product run during the next. The cache slot of
-// a row follows from q_starts, the lengths and the page table; each epilogue thread looks
-// its own row's up while the operands are on their way. One more CTA per 128 rows copies the
-// latent rows and the RoPE keys.
+// A CTA pair (cta_group::2) takes 256 rows and a share of the groups: each CTA holds its 128
+// rows of A (K-major, 128 KB) for all of them and streams one half of B_g (rank 0 W_UK_g,
+// rank 1 W_UV_g; MN-major, the weights as stored) through a ring of 64-row slabs, so that
+// the weights cross from L2 once per 256 rows; two 256-column TMEM accumulators let the
+// epilogue of group g run during the products of g + 1. The cache slot of a row follows from
+// q_starts, the lengths and the page table; the threads look theirs up while the operands are
+// on their way. Two warps copy the latent rows and the RoPE keys.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -25,27 +25,29 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kApRows = 128;               // rows per tile (MMA M)
-constexpr int kApThreads = 192;
+constexpr int kApRows = 128;               // rows of one CTA
+constexpr int kApThreads = 384;
 constexpr int kApBoxA = kApRows * 128;     // [128 rows][64 latent columns]
 constexpr int kApA = 8 * kApBoxA;
-constexpr int kApSlab = 32;                // K rows of B per ring stage
-constexpr int kApBoxB = kApSlab * 128;     // [32 K rows][64 columns]
+constexpr int kApSlab = 64;                // K rows of B per ring stage
+constexpr int kApBoxB = kApSlab * 128;     // [64 K rows][64 columns]
+constexpr int kApStage = 2 * kApBoxB;      // one CTA's 128 columns
+constexpr int kApStages = 4;
 constexpr int kApSlabs = kLatent / kApSlab;
+constexpr int kApCopyRows = 16;            // rows copied at a time by the two copying warps
+constexpr int kApCopyBytes = kApCopyRows / 2 * kRow * 2;  // one warp's
 
-template <int NC>
 struct ApSmem {
-    static constexpr int kStage = NC / 64 * kApBoxB;
-    static constexpr int kStages = 4 * 256 / NC;
     static constexpr int oA = 0;
     static constexpr int oB = oA + kApA;
-    static constexpr int oBar = oB + kStages * kStage;
-    // a_full[8], b_full/b_empty[kStages], acc_full/acc_empty[2], drain
-    static constexpr int kNumBars = 8 + 2 * kStages + 4 + 1;
+    static constexpr int oCopy = oB + kApStages * kApStage;
+    static constexpr int oBar = oCopy + 2 * kApCopyBytes;
+    // a_full[8], b_full/b_empty[kApStages], acc_full/acc_empty[2], drain, copy[2]
+    static constexpr int kNumBars = 8 + 2 * kApStages + 4 + 1 + 2;
     static constexpr int oMisc = oBar + kNumBars * 8;
     static constexpr int kAlloc = oMisc + 16 + 1024;
 };
-static_assert(ApSmem<256>::kAlloc <= 227 * 1024 && ApSmem<128>::kAlloc <= 227 * 1024, "shared memory");
+static_assert(ApSmem::kAlloc <= 227 * 1024, "shared memory");
 
 struct ApParams {
     const uint4 *rows;            // [total][576] bf16
@@ -56,7 +58,7 @@ struct ApParams {
     void *ws;
     int64_t total, num_slots;
     int batch, max_pages, num_pages;
-    int products;                 // products (of NC columns) of one CTA
+    int groups;                   // groups of one pair
 };
 
 // Cache slot of row r, or -1 if it belongs to no (valid) sequence or its page is outside the
@@ -79,57 +81,88 @@ __device__ int64_t ap_slot(const ApParams &p, int64_t r, bool report) {
     return (int64_t)page * kPage + t % kPage;
 }
 
-// The copying CTA of a tile: its rows' latent rows and RoPE keys, 16 bytes a thread.
-__device__ void ap_copy(const ApParams &p, int64_t row0) {
-    __shared__ int64_t slot[kApRows];
-    const int tid = threadIdx.x;
-    if (blockIdx.x == 0)
-        for (int b = tid; b < p.batch; b += kApThreads)
+// One warp of two: this CTA's share of its tile's latent rows and RoPE keys, eight rows at a
+// time through shared memory by bulk copies (one in, one or two out per row). Row by row
+// through registers the copies took twice as long as the products beside them.
+__device__ __forceinline__ void ap_copy(const ApParams &p, int64_t row0, int w, uint8_t *stage, uint64_t *bar,
+                                        volatile int *abort_flag) {
+    constexpr int kRowBytes = kRow * 2;
+    const int lane = threadIdx.x & 31;
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int b = 32 * w + lane; b < p.batch; b += 64)
             if (ragged_seq(p.q_starts, p.seqlens, b, p.total, p.max_pages).bad) report_error(p.ws, GQLA_ERR_DEVICE, b);
-    if (tid < kApRows) slot[tid] = row0 + tid < p.total ? ap_slot(p, row0 + tid, true) : -1;
-    __syncthreads();
-    constexpr int kChunks = kRow / 8, kFirstRope = kLatent / 8;  // 16-byte pieces of a row
-    const int lead = p.latent ? 0 : kFirstRope;                  // without a latent cache: the RoPE keys only
-    const int per = kChunks - lead;
-#pragma unroll 4
-    for (int i = tid; i < kApRows * per; i += kApThreads) {
-        const int r = i / per, ch = lead + i % per;
-        const int64_t s = slot[r];
-        if (s < 0) continue;
-        const uint4 v = p.rows[(row0 + r) * kChunks + ch];
-        if (p.latent) p.latent[s * kChunks + ch] = v;
-        if (p.k_rope && ch >= kFirstRope) p.k_rope[s * (kRope / 8) + ch - kFirstRope] = v;
+    uint32_t n = 0;
+    for (int r0 = blockIdx.y * kApCopyRows; r0 < kApRows; r0 += gridDim.y * kApCopyRows, ++n) {
+        const int64_t r = row0 + r0 + w * kApCopyRows / 2;
+        const int rows = (int)min((int64_t)kApCopyRows / 2, p.total - r);
+        if (rows <= 0) break;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, rows * kRowBytes);
+            bulk_load(stage, reinterpret_cast<const uint8_t *>(p.rows) + r * kRowBytes, rows * kRowBytes, bar);
+        }
+        const int64_t s = lane < rows ? ap_slot(p, r + lane, true) : -1;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar, n & 1, abort_flag))) {
+            *abort_flag = 1;
+            break;
+        }
+        if (s >= 0) {
+            const uint8_t *row = stage + lane * kRowBytes;
+            if (p.latent) bulk_store(reinterpret_cast<uint8_t *>(p.latent) + s * kRowBytes, row, kRowBytes);
+            if (p.k_rope) bulk_store(reinterpret_cast<uint8_t *>(p.k_rope) + s * kRope * 2, row + kLatent * 2, kRope * 2);
+        }
+        bulk_commit_group();
+        bulk_wait_group_read<0>();
+        __syncwarp();
     }
+    bulk_wait_group<0>();
 }
 
-template <int NC>
-__global__ void __launch_bounds__(kApThreads, 1)
+// Latent cache only (no expansion).
+__global__ void __launch_bounds__(64) append_latent_kernel(const ApParams p) {
+    __shared__ __align__(128) uint8_t stage[2][kApCopyBytes];
+    __shared__ uint64_t bar[2];
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar[0], 1);
+        mbar_init(&bar[1], 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int w = threadIdx.x >> 5;
+    ap_copy(p, (int64_t)blockIdx.x * kApRows, w, stage[w], &bar[w], &abort_flag);
+    __syncthreads();
+    if (threadIdx.x == 0 && abort_flag) report_error(p.ws, GQLA_ERR_TIMEOUT, (int)blockIdx.x);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
     append_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant__ CUtensorMap wuk_map,
                   const __grid_constant__ CUtensorMap wuv_map, const ApParams p) {
-    using SM = ApSmem<NC>;
-    constexpr int ST = SM::kStages;
+    using SM = ApSmem;
+    constexpr int ST = kApStages;
     const int64_t row0 = (int64_t)blockIdx.x * kApRows;
-    if (blockIdx.y == 0) {  // one CTA of a tile copies
-        griddep_wait();
-        griddep_launch_dependents();
-        ap_copy(p, row0);
-        return;
-    }
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *a_full = reinterpret_cast<uint64_t *>(smem + SM::oBar);
     uint64_t *b_full = a_full + 8, *b_empty = b_full + ST, *acc_full = b_empty + ST, *acc_empty = acc_full + 2;
-    uint64_t *drain = acc_empty + 2;
+    uint64_t *drain = acc_empty + 2, *copy_bar = drain + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::oMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::oMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = (blockIdx.y - 1) * p.products;  // this CTA's first product: group first * NC / 256
+    const uint32_t rank = cluster_rank();
+    const int g0 = blockIdx.y * p.groups;  // this pair's first group
+    // the barriers that the MMA issuer waits for are those of rank 0
+    auto lead = [](uint64_t *bar) { return map_peer(smem_u32(bar), 0); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 8; ++i) mbar_init(&a_full[i], 1);
         for (int i = 0; i < ST; ++i) { mbar_init(&b_full[i], 1); mbar_init(&b_empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 16); }
         mbar_init(drain, 1);
+        mbar_init(&copy_bar[0], 1);
+        mbar_init(&copy_bar[1], 1);
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&row_map);
@@ -137,11 +170,12 @@ __global__ void __launch_bounds__(kApThreads, 1)
         prefetch_tensormap(&wuv_map);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
         tc_fence_before();
     }
     __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
@@ -150,118 +184,118 @@ __global__ void __launch_bounds__(kApThreads, 1)
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
         if (elect_one()) {
-            int u = 0, boxes = 0;
-            for (int x = 0; x < p.products && !*abort_flag; ++x) {
-                const int col = (first + x) * NC % kKv, wrow = (first + x) * NC / kKv * kLatent;
+            const CUtensorMap *w_map = rank ? &wuv_map : &wuk_map;
+            int u = 0;
+            for (int x = 0; x < p.groups && !*abort_flag; ++x)
                 for (int kb = 0; kb < kApSlabs; ++kb, ++u) {
-                    // A with the first product's B, two slabs of B to a box of A
-                    if (x == 0 && kb % 2 == 0) {
-                        mbar_arrive_expect_tx(&a_full[kb / 2], kApBoxA);
-                        tma_load_2d(smem + SM::oA + kb / 2 * kApBoxA, &row_map, &a_full[kb / 2], 32 * kb, (int)row0);
-                        ++boxes;
+                    if (x == 0) {  // a box of A with each slab of the first group
+                        if (rank == 0) mbar_arrive_expect_tx(&a_full[kb], 2 * kApBoxA);
+                        tma_load_2d_pair(smem + SM::oA + kb * kApBoxA, &row_map, lead(&a_full[kb]), 64 * kb, (int)row0);
                     }
                     const int st = u % ST;
                     if (!mbar_wait(&b_empty[st], ((u / ST) & 1) ^ 1, abort_flag)) *abort_flag = 1;
                     if (*abort_flag) break;
-                    uint8_t *dst = smem + SM::oB + st * SM::kStage;
-                    mbar_arrive_expect_tx(&b_full[st], SM::kStage);
-                    const int y = wrow + kb * kApSlab;
-#pragma unroll
-                    for (int h = 0; h < NC / 64; ++h) {
-                        const int cc = col + 64 * h;
-                        tma_load_2d(dst + h * kApBoxB, cc < kNope ? &wuk_map : &wuv_map, &b_full[st], cc % kNope, y);
-                    }
+                    uint8_t *dst = smem + SM::oB + st * kApStage;
+                    if (rank == 0) mbar_arrive_expect_tx(&b_full[st], 2 * kApStage);
+                    const int y = (g0 + x) * kLatent + kb * kApSlab;
+                    tma_load_2d_pair(dst, w_map, lead(&b_full[st]), 0, y);
+                    tma_load_2d_pair(dst + kApBoxB, w_map, lead(&b_full[st]), 64, y);
                 }
-            }
-            // never leave with copies in flight
-            int dummy = 0;
-            volatile int *no_abort = reinterpret_cast<volatile int *>(&dummy);
-            for (int i = u > ST ? u - ST : 0; i < u; ++i) mbar_wait(&b_full[i % ST], (i / ST) & 1, no_abort);
-            for (int i = 0; i < boxes; ++i) mbar_wait(&a_full[i], 0, no_abort);
+            // every copy has been used, and the other CTA's commits have arrived here
+            for (int i = u > ST ? u - ST : 0; i < u && !*abort_flag; ++i)
+                if (!mbar_wait(&b_empty[i % ST], (i / ST) & 1, abort_flag)) *abort_flag = 1;
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
-        if (elect_one()) {
-            constexpr uint32_t idesc = idesc_bf16(kApRows, NC, 0, 1);
-            const uint64_t a_d0 = smem_desc(smem_u32(smem + SM::oA), 16, 1024, kSw128);
-            const uint64_t b_d0 = smem_desc(smem_u32(smem + SM::oB), kApBoxB, 1024, kSw128);
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t idesc = idesc_bf16(2 * kApRows, 256, 0, 1);
+            // A K-major, 64-column boxes; B MN-major, two atoms of 64 columns in each CTA
+            const uint64_t a_d = smem_desc(smem_u32(smem + SM::oA), kApBoxB, 1024, kSw128);
+            const uint32_t b_lo0 = static_cast<uint32_t>(smem_desc(smem_u32(smem + SM::oB), kApBoxB, 1024, kSw128));
+            const uint32_t a_lo = static_cast<uint32_t>(a_d), hi = static_cast<uint32_t>(a_d >> 32);
             int u = 0;
-            for (int x = 0; x < p.products && !*abort_flag; ++x) {
+            for (int x = 0; x < p.groups && !*abort_flag; ++x) {
                 const int ab = x & 1;
                 if (!mbar_wait(&acc_empty[ab], ((x >> 1) & 1) ^ 1, abort_flag)) *abort_flag = 1;
                 for (int kb = 0; kb < kApSlabs; ++kb, ++u) {
                     const int st = u % ST;
-                    if (x == 0 && !mbar_wait(&a_full[kb / 2], 0, abort_flag)) *abort_flag = 1;
-                    if (!mbar_wait(&b_full[st], (u / ST) & 1, abort_flag)) *abort_flag = 1;
+                    bool ok = x > 0 || mbar_wait(&a_full[kb], 0, abort_flag);
+                    ok = ok && mbar_wait(&b_full[st], (u / ST) & 1, abort_flag);
+                    if (!ok) *abort_flag = 1;
                     tc_fence_after();
-                    if (!*abort_flag) {
+                    const uint32_t a = a_lo + (kb * kApBoxA >> 4), b = b_lo0 + (st * kApStage >> 4);
 #pragma unroll
-                        for (int ks = 0; ks < kApSlab / 16; ++ks) {
-                            const int k = kb * kApSlab + ks * 16;
-                            mma_bf16(tmem + 256 * ab, desc_advance(a_d0, (k >> 6) * kApBoxA + ((k & 63) >> 3) * 16),
-                                     desc_advance(b_d0, st * SM::kStage + ks * 16 * 128), idesc,
-                                     (kb > 0 || ks > 0) ? 1u : 0u);
-                        }
-                    }
-                    mma_commit(&b_empty[st]);
+                    for (int ks = 0; ks < kApSlab / 16; ++ks)
+                        mma_bf16_pair(tmem + 256 * ab, a + (ks * 32 >> 4), b + (ks * 2048 >> 4), hi, idesc,
+                                      (kb > 0 || ks > 0) ? 1u : 0u);
+                    mma_commit_pair(&b_empty[st]);
                 }
-                mma_commit(&acc_full[ab]);
+                mma_commit_pair(&acc_full[ab]);
             }
-            mma_commit(drain);
+            mma_commit_pair(drain, 1);
             int dummy = 0;
             mbar_wait(drain, 0, reinterpret_cast<volatile int *>(&dummy));
         }
-    } else {
+    } else if (warp >= 4) {
         // ---------------------------------------------------------------- epilogue
-        const int quad = warp & 3;
+        // two warps to a TMEM lane quadrant, one for K_nope's columns and one for V's
+        const int quad = warp & 3, col0 = (warp - 4) >> 2 ? kNope : 0;
         const int64_t r = row0 + 32 * quad + lane;
         const uint32_t lane_off = static_cast<uint32_t>(32 * quad) << 16;
         const int64_t slot = r < p.total ? ap_slot(p, r, false) : -1;
-        for (int x = 0; x < p.products; ++x) {
+        // four lanes trade 16-byte units, so that they write 64 bytes of one row together
+        int64_t to[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, slot, (lane & ~3) + k);
+        for (int x = 0; x < p.groups; ++x) {
             const int ab = x & 1;
             if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ab], (x >> 1) & 1, abort_flag))) {
                 *abort_flag = 1;
                 break;
             }
             tc_fence_after();
-            const int col = (first + x) * NC % kKv, g = (first + x) * NC / kKv;
-            uint4 *dst = reinterpret_cast<uint4 *>(p.kv + ((int64_t)g * p.num_slots + slot) * kKv + col);
-#pragma unroll 1
-            for (int cc = 0; cc < NC; cc += 32) {
-                uint32_t v[32];
+            __nv_bfloat16 *base = p.kv + (int64_t)(g0 + x) * p.num_slots * kKv + (lane & 3) * 8;
+#pragma unroll 2
+            for (int cc = col0; cc < col0 + kNope; cc += 32) {
+                uint32_t v[32], w[16];
                 tmem_ld32(tmem + 256 * ab + lane_off + cc, v);
                 tmem_wait_ld();
-                if (slot < 0) continue;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint2 lo = pack_bf16x4(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1]),
-                                                 __uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]));
-                    const uint2 hi = pack_bf16x4(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]),
-                                                 __uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]));
-                    dst[cc / 8 + i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                for (int i = 0; i < 16; ++i) {
+                    __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    w[i] = *reinterpret_cast<uint32_t *>(&t);
                 }
+                quad_transpose(w, lane);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (to[k] >= 0)
+                        *reinterpret_cast<uint4 *>(base + to[k] * kKv + cc) =
+                            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[ab]);
+            if (lane == 0) mbar_arrive_remote_relaxed(lead(&acc_empty[ab]));
         }
+    } else {
+        ap_copy(p, row0, warp - 2, smem + SM::oCopy + (warp - 2) * kApCopyBytes, &copy_bar[warp - 2], abort_flag);
     }
+    // Leave together: as in prefill.cu, after the first barrier neither CTA sends anything new
     tc_fence_before();
     __syncthreads();
-    if (*abort_flag && threadIdx.x == 0) report_error(p.ws, GQLA_ERR_TIMEOUT, (int)blockIdx.x);
+    if (threadIdx.x == 0 && *abort_flag) {
+        report_error(p.ws, GQLA_ERR_TIMEOUT, (int)blockIdx.x);
+        st_cluster_b32(map_peer(smem_u32(const_cast<int *>(abort_flag)), rank ^ 1), 1);
+    }
+    cluster_sync();
+    if (*abort_flag) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < 200000) {}
+    }
+    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc_pair(tmem, 512);
     }
-}
-
-template <int NC>
-cudaError_t launch_append_nc(const CUtensorMap &rm, const CUtensorMap &wuk, const CUtensorMap &wuv, const ApParams &p,
-                             dim3 grid, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(append_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         ApSmem<NC>::kAlloc);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(append_kernel<NC>, grid, dim3(kApThreads), ApSmem<NC>::kAlloc, stream, rm, wuk, wuv, p);
 }
 
 }  // namespace
@@ -283,10 +317,10 @@ cudaError_t launch_append(const void *rows, int64_t total, const int32_t *q_star
     p.batch = idx->batch;
     p.max_pages = idx->max_pages_per_seq;
     p.num_pages = idx->num_pages;
-    p.products = 0;
-    CUtensorMap rm = {}, wuk = {}, wuv = {};
+    p.groups = 0;
     const unsigned tiles = (unsigned)((total + kApRows - 1) / kApRows);
-    if (!kv) return launch_append_nc<256>(rm, wuk, wuv, p, dim3(tiles, 1), stream);
+    if (!kv) return launch_dependent(append_latent_kernel, dim3(tiles, 8), dim3(64), 0, stream, p);
+    CUtensorMap rm, wuk, wuv;
     {
         const uint64_t dims[2] = {(uint64_t)kRow, (uint64_t)total};
         const uint64_t strides[1] = {(uint64_t)kRow * 2};
@@ -303,16 +337,16 @@ cudaError_t launch_append(const void *rows, int64_t total, const int32_t *q_star
     }
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // Few tiles: a CTA per 128 output columns, so that the weights' 2 MB are read by as many
-    // SMs as there are; otherwise a CTA takes whole groups, as many as leave one wave.
-    if ((int64_t)tiles * 2 * num_groups <= sms) {
-        p.products = 1;
-        return launch_append_nc<128>(rm, wuk, wuv, p, dim3(tiles, 1 + 2 * num_groups), stream);
-    }
+    // the groups over as many pairs as one wave holds: few rows read the weights' 2 MB through
+    // many SMs
+    const int64_t pairs = (tiles + 1) / 2;
     int split = 1;
-    while (split * 2 <= num_groups && num_groups % (split * 2) == 0 && (int64_t)tiles * split * 2 <= sms) split *= 2;
-    p.products = num_groups / split;
-    return launch_append_nc<256>(rm, wuk, wuv, p, dim3(tiles, 1 + split), stream);
+    while (split * 2 <= num_groups && num_groups % (split * 2) == 0 && pairs * split * 2 <= sms / 2) split *= 2;
+    p.groups = num_groups / split;
+    cudaError_t e = cudaFuncSetAttribute(append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ApSmem::kAlloc);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(append_kernel, dim3((unsigned)(2 * pairs), split), dim3(kApThreads), ApSmem::kAlloc, stream,
+                            rm, wuk, wuv, p);
 }
 
 }  // namespace gqla

@@ -86,19 +86,6 @@ __device__ __forceinline__ int ld_cluster_b32(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
-                 "r"(smem_u32(src)), "r"(bytes)
-                 : "memory");
-}
-
 // Where piece `x` of page `page` lies.
 __device__ __forceinline__ uint8_t *piece_ptr(const CpParams &p, int x, int64_t page) {
     if (x < p.lat_pieces) return p.latent + (page * kLatPieces + x) * kCpPiece;

@@ -327,25 +327,6 @@ __device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, 
     return t.x + t.y;
 }
 
-// Four 16-byte units of each of four neighbouring lanes, transposed: lane j of the four ends
-// with unit j of lane k in its place k.
-__device__ __forceinline__ void quad_transpose(uint32_t (&w)[16], int lane) {
-#pragma unroll
-    for (int b = 1; b <= 2; b <<= 1) {
-        const bool up = (lane & b) != 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (u & b) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[4 * u + e] : w[4 * (u | b) + e], b);
-                if (up) w[4 * u + e] = got;
-                else w[4 * (u | b) + e] = got;
-            }
-        }
-    }
-}
-
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     prefill_gqa_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap kr_map,
                        const __grid_constant__ CUtensorMap q_map, const PfParams p) {

@@ -221,6 +221,21 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
                  : "memory");
 }
 
+// Untiled bulk copies (16-byte aligned, a multiple of 16 bytes): into shared memory, completing
+// on an mbarrier of this CTA, and out of it, tracked by the issuing thread's bulk groups.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+                 "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit_group() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -604,6 +619,27 @@ __device__ __forceinline__ __half2 fast_exp2_h2(__half2 x) {
     uint32_t y;
     asm("ex2.approx.f16x2 %0, %1;" : "=r"(y) : "r"(*reinterpret_cast<uint32_t *>(&x)));
     return *reinterpret_cast<__half2 *>(&y);
+}
+
+// ------------------------------------------------------------------ registers
+
+// Four 16-byte units of each of four neighbouring lanes, transposed: lane j of the four ends
+// with unit j of lane k in its place k.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[16], int lane) {
+#pragma unroll
+    for (int b = 1; b <= 2; b <<= 1) {
+        const bool up = (lane & b) != 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (u & b) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[4 * u + e] : w[4 * (u | b) + e], b);
+                if (up) w[4 * u + e] = got;
+                else w[4 * (u | b) + e] = got;
+            }
+        }
+    }
 }
 
 // ------------------------------------------------------------------ descriptors
