@@ -343,7 +343,10 @@ cudaError_t launch_append(const void *rows, int64_t total, const int32_t *q_star
     int split = 1;
     while (split * 2 <= num_groups && num_groups % (split * 2) == 0 && pairs * split * 2 <= sms / 2) split *= 2;
     p.groups = num_groups / split;
-    cudaError_t e = cudaFuncSetAttribute(append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ApSmem::kAlloc);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = once_per_device(ready, [] {
+        return cudaFuncSetAttribute(append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ApSmem::kAlloc);
+    });
     if (e != cudaSuccess) return e;
     return launch_dependent(append_kernel, dim3((unsigned)(2 * pairs), split), dim3(kApThreads), ApSmem::kAlloc, stream,
                             rm, wuk, wuv, p);

@@ -537,8 +537,11 @@ cudaError_t launch_copy_pages(const int32_t *pairs, int64_t n, int num_pages, in
     p.pieces = p.lat_pieces + p.kv_pieces + (k_rope ? 1 : 0);
     p.words = (num_pages + 31) / 32;
     const int bytes = kCpStages * kCpPiece + 2 * p.words * 4;
-    cudaError_t e = cudaFuncSetAttribute(copy_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kCpStages * kCpPiece + 2 * (kCpMaxPages / 32) * 4);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = once_per_device(ready, [] {
+        return cudaFuncSetAttribute(copy_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kCpStages * kCpPiece + 2 * (kCpMaxPages / 32) * 4);
+    });
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -551,7 +554,10 @@ cudaError_t launch_fork(const gqla_page_pool *pool, const int32_t *forks, int n,
                         cudaStream_t stream) {
     FkParams p{make_pool(pool, ws), reinterpret_cast<const int2 *>(forks), reinterpret_cast<int2 *>(pairs), n};
     const int bytes = 2 * ((pool->batch + 31) / 32) * 4 + n;
-    cudaError_t e = cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = once_per_device(ready, [] {
+        return cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    });
     if (e != cudaSuccess) return e;
     return launch_dependent(fork_kernel, dim3(kPgCluster), dim3(kPgThreads), bytes, stream, p);
 }

@@ -900,14 +900,18 @@ cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_
         const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)p.tile_tokens};
         if (!make_bf16_map(&qm, q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
     }
-    cudaError_t e = cudaFuncSetAttribute(prefill_gqa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         PfSmem::kAlloc);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = once_per_device(ready, [] {
+        cudaError_t r = cudaFuncSetAttribute(prefill_gqa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             PfSmem::kAlloc);
+        cudaFuncAttributes fa;
+        if (r == cudaSuccess) r = cudaFuncGetAttributes(&fa, prefill_gqa_kernel);
+        if (r != cudaSuccess) return r;
+        // the register split must not ask for more than the launch gives
+        return 128 * kPfIssueRegs + 256 * kPfSoftmaxRegs > kPfThreads * fa.numRegs ? cudaErrorInvalidConfiguration
+                                                                                     : cudaSuccess;
+    });
     if (e != cudaSuccess) return e;
-    // the register split must not ask for more than the launch gives
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, prefill_gqa_kernel);
-    if (e != cudaSuccess) return e;
-    if (128 * kPfIssueRegs + 256 * kPfSoftmaxRegs > kPfThreads * fa.numRegs) return cudaErrorInvalidConfiguration;
     e = launch_dependent(prefill_gqa_kernel, dim3(2 * num_splits), dim3(kPfThreads), PfSmem::kAlloc, stream, kvm, krm, qm, p);
     if (e != cudaSuccess || num_splits == 1) return e;
     return launch_dependent(prefill_combine_kernel, dim3(num_splits - 1, kPfBlockRows / kPcRows),

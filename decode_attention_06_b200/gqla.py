@@ -324,93 +324,139 @@ def gqla_decode_gqa_noalloc(dims, q, kv_expanded, k_rope, kv, num_splits, out, l
 
 
 # ------------------------------------------------------------------ ragged batches of new tokens
+#
+# The calls from here on may be small (a step's tokens, a few pages), so their marshalling is kept
+# to what the checks need: _ptr instead of _dev, and the raw stream of the tensors' device. They
+# refuse tensors of another device than the current one.
+
+def _ptr(t, name, dtype, shape):
+    """Device address of a contiguous CUDA tensor of this type and shape on the current device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, shape):
+    return None if t is None else _ptr(t, name, dtype, shape)
+
+
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(_current_device())
+
+
+def _ws(workspace):
+    """(address, bytes) of a workspace."""
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if workspace.get_device() != _current_device():
+        raise ValueError("workspace must be on the current device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _index_on_device(idx):
+    for t in idx._keep:
+        if t.get_device() != _current_device():
+            raise ValueError(f"the index is on {t.device}, the current device is cuda:{_current_device()}")
+    return ctypes.byref(idx)
+
 
 def gqla_prefill_gqa(dims, q, q_starts, kv_expanded, k_rope, kv, num_splits, o_part, lse_part, out, lse_out,
                      workspace, stream=None):
     """Attention of chunks of new tokens; o_part / lse_part may be None for one split."""
-    n = kv.num_pages * kv.page_size
-    h, total = dims.num_heads, q.shape[0]
+    n, h, total = kv.num_pages * kv.page_size, dims.num_heads, q.shape[0]
     slots = gqla_prefill_slots(num_splits)
+    bf16, f32 = torch.bfloat16, torch.float32
+    ws, ws_bytes = _ws(workspace)
     _check("gqla_prefill_gqa", _lib.gqla_prefill_gqa(
-        ctypes.byref(dims), _dev(q, "q", torch.bfloat16, (total, h, D_QK)), total,
-        _dev(q_starts, "q_starts", torch.int32, (kv.batch + 1,)),
-        _dev(kv_expanded, "kv_expanded", torch.bfloat16, (dims.num_groups, n, D_NOPE + D_V)),
-        _dev(k_rope, "k_rope", torch.bfloat16, (n, D_ROPE)), n, ctypes.byref(kv), num_splits,
-        None if o_part is None else _dev(o_part, "o_part", torch.float32, (slots, PREFILL_BLOCK_ROWS, D_V)),
-        None if lse_part is None else _dev(lse_part, "lse_part", torch.float32, (slots, PREFILL_BLOCK_ROWS)),
-        _dev(out, "out", torch.bfloat16, (total, h, D_V)),
-        None if lse_out is None else _dev(lse_out, "lse_out", torch.float32, (total, h)),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+        ctypes.byref(dims), _ptr(q, "q", bf16, (total, h, D_QK)), total,
+        _ptr(q_starts, "q_starts", torch.int32, (kv.batch + 1,)),
+        _ptr(kv_expanded, "kv_expanded", bf16, (dims.num_groups, n, D_NOPE + D_V)),
+        _ptr(k_rope, "k_rope", bf16, (n, D_ROPE)), n, _index_on_device(kv), num_splits,
+        _opt(o_part, "o_part", f32, (slots, PREFILL_BLOCK_ROWS, D_V)),
+        _opt(lse_part, "lse_part", f32, (slots, PREFILL_BLOCK_ROWS)),
+        _ptr(out, "out", bf16, (total, h, D_V)), _opt(lse_out, "lse_out", f32, (total, h)),
+        ws, ws_bytes, _raw(stream)))
 
 
 def gqla_append_cache(dims, rows, q_starts, kv, workspace, latent_cache=None, w_uk=None, w_uv=None,
                       kv_expanded=None, k_rope=None, stream=None):
     """The latent rows of new tokens into the caches that are given (latent, expanded + RoPE keys)."""
-    n, total, g = kv.num_pages * kv.page_size, rows.shape[0], dims.num_groups
+    n, total, g, bf16 = kv.num_pages * kv.page_size, rows.shape[0], dims.num_groups, torch.bfloat16
+    ws, ws_bytes = _ws(workspace)
     _check("gqla_append_cache", _lib.gqla_append_cache(
-        ctypes.byref(dims), _dev(rows, "rows", torch.bfloat16, (total, D_ROW)), total,
-        _dev(q_starts, "q_starts", torch.int32, (kv.batch + 1,)),
-        None if w_uk is None else _dev(w_uk, "w_uk", torch.bfloat16, (g, D_LATENT, D_NOPE)),
-        None if w_uv is None else _dev(w_uv, "w_uv", torch.bfloat16, (g, D_LATENT, D_V)),
-        *_caches(dims, kv.num_pages, latent_cache, kv_expanded, k_rope), n, ctypes.byref(kv),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+        ctypes.byref(dims), _ptr(rows, "rows", bf16, (total, D_ROW)), total,
+        _ptr(q_starts, "q_starts", torch.int32, (kv.batch + 1,)),
+        _opt(w_uk, "w_uk", bf16, (g, D_LATENT, D_NOPE)), _opt(w_uv, "w_uv", bf16, (g, D_LATENT, D_V)),
+        *_caches(dims, kv.num_pages, latent_cache, kv_expanded, k_rope), n, _index_on_device(kv),
+        ws, ws_bytes, _raw(stream)))
 
 
 # ------------------------------------------------------------------ the pages of a cache
 
 def _caches(dims, num_pages, latent_cache, kv_expanded, k_rope):
-    n = num_pages * PAGE_SIZE
-    return (None if latent_cache is None else
-            _dev(latent_cache, "latent_cache", torch.bfloat16, (num_pages, PAGE_SIZE, D_ROW)),
-            None if kv_expanded is None else
-            _dev(kv_expanded, "kv_expanded", torch.bfloat16, (dims.num_groups, n, D_NOPE + D_V)),
-            None if k_rope is None else _dev(k_rope, "k_rope", torch.bfloat16, (n, D_ROPE)))
-
-
-def _pairs(t, name, rows=None):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] != 2 or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be [{'n' if rows is None else rows}][2]")
-    return _dev(t, name, torch.int32)
+    n, bf16 = num_pages * PAGE_SIZE, torch.bfloat16
+    return (_opt(latent_cache, "latent_cache", bf16, (num_pages, PAGE_SIZE, D_ROW)),
+            _opt(kv_expanded, "kv_expanded", bf16, (dims.num_groups, n, D_NOPE + D_V)),
+            _opt(k_rope, "k_rope", bf16, (n, D_ROPE)))
 
 
 def gqla_copy_pages(dims, pairs, num_pages, workspace, latent_cache=None, kv_expanded=None, k_rope=None, stream=None):
     """Pages pairs[i] = (source, target) of the given caches; a negative source is skipped."""
+    ws, ws_bytes = _ws(workspace)
+    n = pairs.shape[0]
     _check("gqla_copy_pages", _lib.gqla_copy_pages(
-        ctypes.byref(dims), _pairs(pairs, "pairs"), pairs.shape[0], num_pages,
-        *_caches(dims, num_pages, latent_cache, kv_expanded, k_rope),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+        ctypes.byref(dims), _ptr(pairs, "pairs", torch.int32, (n, 2)), n, num_pages,
+        *_caches(dims, num_pages, latent_cache, kv_expanded, k_rope), ws, ws_bytes, _raw(stream)))
 
 
 def gqla_fork_sequences(pool, forks, pairs, workspace, stream=None):
     """forks[i] = (parent, child); pairs[i] receives the page copy that the fork needs, or (-1, -1)."""
+    ws, ws_bytes = _ws(workspace)
+    n = forks.shape[0]
     _check("gqla_fork_sequences", _lib.gqla_fork_sequences(
-        ctypes.byref(pool), _pairs(forks, "forks"), forks.shape[0], _pairs(pairs, "pairs", forks.shape[0]),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _index_on_device(pool), _ptr(forks, "forks", torch.int32, (n, 2)), n,
+        _ptr(pairs, "pairs", torch.int32, (n, 2)), ws, ws_bytes, _raw(stream)))
 
 
 def gqla_extend_sequences(pool, new_tokens, workspace, stream=None):
     """new_tokens[b] more tokens (and the pages for them) for every sequence."""
+    ws, ws_bytes = _ws(workspace)
     _check("gqla_extend_sequences", _lib.gqla_extend_sequences(
-        ctypes.byref(pool), _dev(new_tokens, "new_tokens", torch.int32, (pool.batch,)),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _index_on_device(pool), _ptr(new_tokens, "new_tokens", torch.int32, (pool.batch,)), ws, ws_bytes, _raw(stream)))
 
 
 def gqla_free_sequences(pool, seq_ids, workspace, stream=None):
-    if seq_ids.dim() != 1:
-        raise ValueError("seq_ids must be [n]")
+    """The pages of the listed sequences lose one reference each; their lengths become 0."""
+    ws, ws_bytes = _ws(workspace)
+    n = seq_ids.shape[0]
     _check("gqla_free_sequences", _lib.gqla_free_sequences(
-        ctypes.byref(pool), _dev(seq_ids, "seq_ids", torch.int32), seq_ids.shape[0],
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _index_on_device(pool), _ptr(seq_ids, "seq_ids", torch.int32, (n,)), n, ws, ws_bytes, _raw(stream)))
 
 
 def gqla_compact_pages(pool, page_table_out, page_refs_out, pairs, counts, workspace, stream=None):
     """Live pages to the front; pairs receives the moves (gqla_copy_pages), counts = (live pages, moves).
     The outputs may be the pool's own tables."""
+    ws, ws_bytes = _ws(workspace)
+    i32 = torch.int32
     _check("gqla_compact_pages", _lib.gqla_compact_pages(
-        ctypes.byref(pool), _dev(page_table_out, "page_table_out", torch.int32, (pool.batch, pool.max_pages_per_seq)),
-        _dev(page_refs_out, "page_refs_out", torch.int32, (pool.num_pages,)),
-        _pairs(pairs, "pairs", max(1, pool.num_pages // 2)), _dev(counts, "counts", torch.int32, (2,)),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _index_on_device(pool), _ptr(page_table_out, "page_table_out", i32, (pool.batch, pool.max_pages_per_seq)),
+        _ptr(page_refs_out, "page_refs_out", i32, (pool.num_pages,)),
+        _ptr(pairs, "pairs", i32, (max(1, pool.num_pages // 2), 2)), _ptr(counts, "counts", i32, (2,)),
+        ws, ws_bytes, _raw(stream)))
 
 
 # ------------------------------------------------------------------ helpers
