@@ -39,7 +39,7 @@ cudaError_t launch_combine(const gqla_kv_index *kv, int s_q, int num_splits, int
                            cudaStream_t stream);
 cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_starts, int heads, int num_groups,
                                const void *kv, const void *k_rope, int64_t num_slots, const gqla_kv_index *idx,
-                               int num_splits, float scale, float *o_part, float *lse_part, void *out,
+                               int num_splits, bool whole, float scale, float *o_part, float *lse_part, void *out,
                                float *lse_out, void *ws, cudaStream_t stream);
 cudaError_t launch_append(const void *rows, int64_t total, const int32_t *q_starts, const void *w_uk,
                           const void *w_uv, int num_groups, void *latent, void *kv, void *k_rope, int64_t num_slots,
@@ -62,6 +62,10 @@ using namespace gqla;
 namespace {
 
 constexpr size_t kWorkspaceBytes = 256;
+
+// gqla_plan_prefill, in the plan's cost units (about a microsecond): the shortest chunk that
+// a block is divided for, the merge's launch and run, and the most blocks that are walked.
+constexpr int64_t kMinChunk = 8, kMergeCost = 5, kMaxWalk = 4096;
 
 bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -477,24 +481,57 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
 }
 
 int gqla_prefill_slots(int num_splits) {
-    if (num_splits <= 0 || num_splits > 65535) return GQLA_ERR_INVALID_ARG;
+    if (num_splits == 0 || num_splits < -65535 || num_splits > 65535) return GQLA_ERR_INVALID_ARG;
+    if (num_splits <= 1) return 0;  // nothing is divided
     return 2 * num_splits + (num_splits + 127) / 128;  // the last ones: 16-byte merge records
 }
 
 int gqla_plan_prefill(const gqla_dims *dims, const int32_t *new_tokens, const int32_t *seqlens, int batch,
-                      int max_splits) {
+                      int max_splits, int *num_splits) {
     const int st = check_ragged_dims(dims);
     if (st != GQLA_OK) return st;
-    if (!new_tokens || !seqlens || batch <= 0 || batch > 65535 || max_splits <= 0 || max_splits > 65535)
+    if (!new_tokens || !seqlens || !num_splits || batch <= 0 || batch > 65535 || max_splits <= 0 || max_splits > 65535)
         return GQLA_ERR_INVALID_ARG;
-    const int T = pf_tile_tokens(dims->num_heads / dims->num_groups);
-    int64_t total = 0;
+    const int T = pf_tile_tokens(dims->num_heads / dims->num_groups), W = 4 * T, g = dims->num_groups;
+    int64_t total = 0, blocks = 0;
     for (int b = 0; b < batch; ++b) {
-        if (new_tokens[b] < 0 || seqlens[b] < new_tokens[b]) return GQLA_ERR_INVALID_ARG;
-        if (new_tokens[b] > 0)
-            total += dims->num_groups * pf_units_before(new_tokens[b], seqlens[b], T, pf_blocks(new_tokens[b], T));
+        const int n = new_tokens[b], L = seqlens[b];
+        if (n < 0 || L < n) return GQLA_ERR_INVALID_ARG;
+        if (n == 0) continue;
+        total += g * pf_units_before(n, L, T, pf_blocks(n, T));
+        blocks += (int64_t)g * pf_blocks(n, T);
     }
-    return (int)std::max<int64_t>(1, std::min<int64_t>(max_splits, total));
+    if (total == 0) {
+        *num_splits = -1;
+        return GQLA_OK;
+    }
+    // Divided: equal chunks, none below kMinChunk units (a piece of a block costs about as much
+    // as a whole one: its start, its end and its partials), then the merge.
+    const int64_t div = std::max<int64_t>(1, std::min<int64_t>(max_splits, total / kMinChunk));
+    const int64_t div_cost = pf_chunk(total, (int)div) + kMergeCost;
+    // Whole blocks: the heaviest chunk, walked through where the blocks are few enough for their
+    // cost to matter.
+    *num_splits = (int)div;
+    if (blocks > kMaxWalk) return GQLA_OK;
+    const int64_t n_whole = std::min<int64_t>(max_splits, blocks);
+    const int64_t k = pf_chunk(total, (int)n_whole);
+    int64_t u = 0, chunk = 0, load = 0, worst = 0;
+    for (int b = 0; b < batch; ++b) {
+        const int n = new_tokens[b], L = seqlens[b], m = pf_blocks(n, T);
+        for (int y = 0; y < g * m; ++y) {
+            const int i = y % m, ntok = std::min(W, n - i * W);
+            const int64_t units = (int64_t)pf_weight(ntok, T) * ((L - n + i * W + ntok + kPfTile - 1) / kPfTile) + kPfBlockCost;
+            if (u / k != chunk) {
+                chunk = u / k;
+                load = 0;
+            }
+            load += units;
+            worst = std::max(worst, load);
+            u += units;
+        }
+    }
+    if (worst <= div_cost || div == 1) *num_splits = -(int)n_whole;
+    return GQLA_OK;
 }
 
 int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, const int32_t *q_starts,
@@ -505,19 +542,20 @@ int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, cons
     if (st != GQLA_OK) return st;
     if ((st = check_index(kv)) != GQLA_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
-    if (total_q < 0 || num_splits <= 0 || num_splits > 65535) return GQLA_ERR_INVALID_ARG;
+    if (total_q < 0 || num_splits == 0 || num_splits < -65535 || num_splits > 65535) return GQLA_ERR_INVALID_ARG;
     if (!q || !q_starts || !kv_expanded || !k_rope || !out) return GQLA_ERR_INVALID_ARG;
-    if (num_splits > 1 && (!o_part || !lse_part)) return GQLA_ERR_INVALID_ARG;
+    const bool whole = num_splits <= 1;
+    if (!whole && (!o_part || !lse_part)) return GQLA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kv_expanded) || !aligned16(k_rope) || !aligned16(out) ||
-        (num_splits > 1 && (!aligned16(o_part) || !aligned16(lse_part))))
+        (!whole && (!aligned16(o_part) || !aligned16(lse_part))))
         return GQLA_ERR_INVALID_ARG;
     if (num_slots != (int64_t)kv->num_pages * kv->page_size) return GQLA_ERR_INVALID_ARG;
     const int64_t most = ((int64_t)1 << 31) - 1;
     if (total_q > most || num_slots > most) return GQLA_ERR_UNSUPPORTED;
     if (total_q == 0) return GQLA_OK;
     return cuda_status(launch_prefill_gqa(q, total_q, q_starts, dims->num_heads, dims->num_groups, kv_expanded,
-                                          k_rope, num_slots, kv, num_splits, dims->softmax_scale, o_part, lse_part,
-                                          out, lse_out, workspace, reinterpret_cast<cudaStream_t>(stream)));
+                                          k_rope, num_slots, kv, std::abs(num_splits), whole, dims->softmax_scale,
+                                          o_part, lse_part, out, lse_out, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int gqla_append_cache(const gqla_dims *dims, const void *rows, int64_t total_q, const int32_t *q_starts,

@@ -26,6 +26,7 @@
 //  * Every wait is bounded; a wait that runs out records GQLA_ERR_TIMEOUT and the CTA
 //    drains and exits.
 #include <cuda.h>
+#include <limits.h>
 
 #include "common.cuh"
 #include "prefill_plan.cuh"
@@ -80,6 +81,7 @@ struct PfParams {
     int64_t total_q;
     int64_t num_slots;
     int batch, max_pages, num_pages, num_splits, heads, groups, G, tile_tokens;
+    bool whole;  // no block is divided: no partials, no merge
     float scale_log2;
 };
 
@@ -180,7 +182,8 @@ __device__ PfPlan pf_plan(const PfParams &p, int c, bool report) {
             off -= pf_units_before(n, L, T, lo);
             r.u0 = pos - off;
             const int w = pf_weight(min(n - lo * 4 * T, 4 * T), T);
-            r.t = (int)((off + w - 1) / w);  // the first tile that starts in the chunk
+            // the first tile of the chunk (past the block's last one: the next block's)
+            r.t = p.whole ? (off > 0 ? INT_MAX : 0) : (int)((off + w - 1) / w);
             return r;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
@@ -233,7 +236,7 @@ struct PfIter {
             o.nt = (o.kv_end + kPfTile - 1) / kPfTile;
             const int w = pf_weight(o.ntok, p.tile_tokens);
             o.t0 = t;
-            o.t1 = (int)min((int64_t)o.nt, (end - u0 + w - 1) / w);
+            o.t1 = p.whole ? o.nt : (int)min((int64_t)o.nt, (end - u0 + w - 1) / w);
             t = 0;
             u0 += (int64_t)w * o.nt + kPfBlockCost;
             if (o.t0 < o.t1) return true;
@@ -582,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     mbar_complete_tx_remote(lead(&v_full[st]), kPfV);
                 }
             }
-            if (p.num_splits > 1 && rank == 0 && lane == 0) *pf_merge(p, c) = merge;
+            if (!p.whole && rank == 0 && lane == 0) *pf_merge(p, c) = merge;
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfSoftmaxRegs));
@@ -858,7 +861,7 @@ __global__ void __launch_bounds__(32 * kPcWarps) prefill_combine_kernel(const Pf
 
 cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_starts, int heads, int num_groups,
                                const void *kv, const void *k_rope, int64_t num_slots, const gqla_kv_index *idx,
-                               int num_splits, float scale, float *o_part, float *lse_part, void *out,
+                               int num_splits, bool whole, float scale, float *o_part, float *lse_part, void *out,
                                float *lse_out, void *ws, cudaStream_t stream) {
     const int G = heads / num_groups;
     PfParams p;
@@ -876,6 +879,7 @@ cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_
     p.max_pages = idx->max_pages_per_seq;
     p.num_pages = idx->num_pages;
     p.num_splits = num_splits;
+    p.whole = whole;
     p.heads = heads;
     p.groups = num_groups;
     p.G = G;
@@ -913,7 +917,7 @@ cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_
     });
     if (e != cudaSuccess) return e;
     e = launch_dependent(prefill_gqa_kernel, dim3(2 * num_splits), dim3(kPfThreads), PfSmem::kAlloc, stream, kvm, krm, qm, p);
-    if (e != cudaSuccess || num_splits == 1) return e;
+    if (e != cudaSuccess || whole) return e;
     return launch_dependent(prefill_combine_kernel, dim3(num_splits - 1, kPfBlockRows / kPcRows),
                             dim3(32 * kPcWarps), 0, stream, p);
 }

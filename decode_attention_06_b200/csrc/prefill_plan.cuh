@@ -14,7 +14,8 @@
 // against a long context spread over many pairs by the same rule. A block that falls in one
 // chunk is finished by its pair; of one that a cut divides, each piece writes a partial (slot
 // 2c: the block began in an earlier chunk; slot 2c + 1: it begins in chunk c and goes on) and
-// the pair that begins it a record of the merge, which the combine carries out.
+// the pair that begins it a record of the merge, which the combine carries out. With `whole`
+// no block is divided: it belongs to the chunk that holds its first unit.
 #pragma once
 
 #include <stdint.h>

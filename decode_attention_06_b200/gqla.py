@@ -81,7 +81,7 @@ _SIGS = {
     "gqla_decode_gqa_noalloc": [_DP, _P, _I, _P, _P, _I64, _KP, _I, _P, _P, _P, _P],
     "gqla_prefill_gqa": [_DP, _P, _I64, _P, _P, _P, _I64, _KP, _I, _P, _P, _P, _P, _P, _SZ, _P],
     "gqla_prefill_slots": [_I],
-    "gqla_plan_prefill": [_DP, _P, _P, _I, _I],
+    "gqla_plan_prefill": [_DP, _P, _P, _I, _I, ctypes.POINTER(ctypes.c_int)],
     "gqla_append_cache": [_DP, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _KP, _P, _SZ, _P],
     "gqla_copy_pages": [_DP, _P, _I64, _I, _P, _P, _P, _P, _SZ, _P],
     "gqla_fork_sequences": [_PP, _P, _I, _P, _P, _SZ, _P],
@@ -376,7 +376,7 @@ def _index_on_device(idx):
 
 def gqla_prefill_gqa(dims, q, q_starts, kv_expanded, k_rope, kv, num_splits, o_part, lse_part, out, lse_out,
                      workspace, stream=None):
-    """Attention of chunks of new tokens; o_part / lse_part may be None for one split."""
+    """Attention of chunks of new tokens; o_part / lse_part are None for num_splits <= 1."""
     n, h, total = kv.num_pages * kv.page_size, dims.num_heads, q.shape[0]
     slots = gqla_prefill_slots(num_splits)
     bf16, f32 = torch.bfloat16, torch.float32
@@ -469,16 +469,17 @@ def gqla_prefill_slots(num_splits: int) -> int:
 
 
 def gqla_plan_prefill(dims, new_tokens, seqlens, max_splits: int) -> int:
-    """Split count of gqla_prefill_gqa for known lengths (host int32 values: CPU tensors or lists)."""
+    """num_splits of gqla_prefill_gqa for known lengths (host int32 values: CPU tensors or lists);
+    negative where no block is divided."""
     new = torch.as_tensor(new_tokens, dtype=torch.int32, device="cpu").contiguous()
     lens = torch.as_tensor(seqlens, dtype=torch.int32, device="cpu").contiguous()
     if new.shape != lens.shape or new.dim() != 1:
         raise ValueError("new_tokens and seqlens must be [batch]")
-    n = _lib.gqla_plan_prefill(ctypes.byref(dims), ctypes.c_void_p(new.data_ptr()), ctypes.c_void_p(lens.data_ptr()),
-                               lens.numel(), max_splits)
-    if n < 0:
-        raise GqlaError("gqla_plan_prefill", n)
-    return n
+    n = ctypes.c_int(0)
+    _check("gqla_plan_prefill", _lib.gqla_plan_prefill(
+        ctypes.byref(dims), ctypes.c_void_p(new.data_ptr()), ctypes.c_void_p(lens.data_ptr()), lens.numel(),
+        max_splits, ctypes.byref(n)))
+    return n.value
 
 
 def plan_prefill(dims, new_tokens, seqlens) -> int:
@@ -615,7 +616,7 @@ class PrefillBuffers:
         h, slots = dims.num_heads, gqla_prefill_slots(num_splits)
         self.num_splits = num_splits
         self.o_part = self.lse_part = None
-        if num_splits > 1:
+        if slots:
             self.o_part = torch.empty(slots, PREFILL_BLOCK_ROWS, D_V, dtype=torch.float32, device=device)
             self.lse_part = torch.empty(slots, PREFILL_BLOCK_ROWS, dtype=torch.float32, device=device)
         self.out = torch.empty(total_q, h, D_V, dtype=torch.bfloat16, device=device)
@@ -629,7 +630,9 @@ def prefill_step(dims, bufs: PrefillBuffers, q, q_starts, kv, kv_expanded, k_rop
     total = q.shape[0]
     if total > bufs.out.shape[0]:
         raise ValueError(f"q has {total} tokens, the buffers hold {bufs.out.shape[0]}")
-    out, lse = bufs.out[:total], bufs.lse[:total]
+    out, lse = bufs.out, bufs.lse
+    if total < out.shape[0]:
+        out, lse = out[:total], lse[:total]
     gqla_prefill_gqa(dims, q, q_starts, kv_expanded, k_rope, kv, bufs.num_splits, bufs.o_part, bufs.lse_part,
                      out, lse, bufs.workspace, stream)
     return out, lse

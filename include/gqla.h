@@ -311,11 +311,14 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
  *   q_starts     device int32 [batch + 1], 0 <= q_starts[b] <= q_starts[b + 1] <= total_q
  *   kv_expanded, k_rope, num_slots, kv   the expanded cache, as for gqla_decode_gqa;
  *                kv->seqlens counts the new tokens
- *   num_splits   C >= 1: the batch's (query block, group, key tile) triples are cut
- *                into C chunks of equal cost, one per CTA pair (gqla_plan_prefill picks C)
+ *   num_splits   the batch's (query block, group, key tile) triples are cut into
+ *                |num_splits| chunks of equal cost, one per CTA pair (1 .. 65535;
+ *                gqla_plan_prefill picks it).  Above 1: a cut may divide a block, whose
+ *                pieces write partials that a second kernel merges.  1 or negative: no
+ *                block is divided, one kernel, no partials
  *   o_part       fp32 [gqla_prefill_slots(C)][512][128], lse_part fp32
- *                [gqla_prefill_slots(C)][512]: partials of the query blocks that a cut
- *                divides; 16-byte aligned; may be NULL when C == 1
+ *                [gqla_prefill_slots(C)][512]: the partials; 16-byte aligned; NULL when
+ *                num_splits <= 1
  *   out          bf16 [total_q][h][128];  lse_out fp32 [total_q][h] or NULL (natural
  *                log, as from gqla_combine).  Rows that belong to no sequence are left
  *                as they were.
@@ -334,15 +337,17 @@ int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, cons
                      void *workspace, size_t workspace_bytes, gqla_stream_t stream);
 
 /* Partial slots (512 rows each) that gqla_prefill_gqa addresses: 2 * num_splits and, for the
- * records of the merge, one more per 128 splits. */
+ * records of the merge, one more per 128 splits; 0 for num_splits <= 1. */
 int gqla_prefill_slots(int num_splits);
 
-/* Host-side choice of gqla_prefill_gqa's num_splits for known lengths.
+/* Host-side choice of gqla_prefill_gqa's num_splits for known lengths: whole blocks where
+ * their heaviest chunk costs no more than an equal share and the merge.
  *   new_tokens, seqlens   host int32 [batch], 0 <= new_tokens[b] <= seqlens[b]
  *   max_splits            1 .. 65535 (half the SM count: one CTA pair for two SMs)
- * Returns the split count, or GQLA_ERR_INVALID_ARG / GQLA_ERR_UNSUPPORTED. */
+ *   num_splits            out
+ * Returns GQLA_OK, GQLA_ERR_INVALID_ARG or GQLA_ERR_UNSUPPORTED.  Host-only. */
 int gqla_plan_prefill(const gqla_dims *dims, const int32_t *new_tokens, const int32_t *seqlens, int batch,
-                      int max_splits);
+                      int max_splits, int *num_splits);
 
 /*
  * Append: the latent rows of new tokens into the pages of the caches, and for the

@@ -128,7 +128,7 @@ SHAPES = {
 
 
 @pytest.mark.parametrize("name", SHAPES)
-@pytest.mark.parametrize("splits", [None, 1, 5, 37])
+@pytest.mark.parametrize("splits", [None, 1, 5, 37, -1, -6, -50])
 def test_prefill_matches_the_formula(name, splits):
     h, g, new, ctx = SHAPES[name]
     c = make(h, g, new, ctx, seed=len(name), gap=3)
