@@ -810,45 +810,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Merge of the divided blocks: CTA (c, y) the rows 32 y .. 32 y + 31 of the block that begins
-// in chunk c, if it goes on: slots 2 c + 1, 2 (c + 1), 2 (c + 2), ... One warp per row, four
-// columns a lane, partials in chunk order.
+// in chunk c, if it goes on: slots 2 c + 1, 2 (c + 1), 2 (c + 2), ... Latency-bound: a warp takes
+// four rows, four columns a lane, and asks for the first two partials of all of them (nearly
+// always there are no more) in one round trip. Partials are added in chunk order.
 // ---------------------------------------------------------------------------
-constexpr int kPcRows = 32, kPcWarps = 8;
+constexpr int kPcRows = 32, kPcWarps = 8, kPcWarpRows = kPcRows / kPcWarps;
 
 __global__ void __launch_bounds__(32 * kPcWarps) prefill_combine_kernel(const PfParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x;
+    const int c = blockIdx.x, r0 = blockIdx.y * kPcRows + warp * kPcWarpRows;
     griddep_wait();
     griddep_launch_dependents();
     const PfMerge mg = *pf_merge(p, c);
-    const int parts = mg.parts;
-    if (parts == 0) return;
-    for (int r = blockIdx.y * kPcRows + warp; r < (int)(blockIdx.y + 1) * kPcRows; r += kPcWarps) {
-        const int in_tile = r % kPfRows;
-        const int tok = r / kPfRows * p.tile_tokens + in_tile / p.G;
-        if (in_tile >= p.tile_tokens * p.G || tok >= mg.ntok) continue;
-        // piece x of the block
-        auto slot = [&](int x) -> int64_t {
-            return (int64_t)(2 * (c + x) + (x == 0 ? 1 : 0)) * kPfBlockRows + r;
-        };
-        float M = -INFINITY;
-        for (int x = lane; x < parts; x += 32) M = fmaxf(M, p.lse_part[slot(x)]);
+    if (mg.parts == 0) return;
+    bool ok[kPcWarpRows];
+    float l0[kPcWarpRows], l1[kPcWarpRows];
+    float4 v0[kPcWarpRows], v1[kPcWarpRows];
+    auto slot = [&](int x) { return (int64_t)(2 * (c + x) + (x == 0 ? 1 : 0)) * kPfBlockRows; };
+    auto load = [&](int64_t row) { return *reinterpret_cast<const float4 *>(p.o_part + row * kDv + 4 * lane); };
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float den = 0.0f;
+    for (int i = 0; i < kPcWarpRows; ++i) {
+        const int in_tile = (r0 + i) % kPfRows;
+        ok[i] = in_tile < p.tile_tokens * p.G && (r0 + i) / kPfRows * p.tile_tokens + in_tile / p.G < mg.ntok;
+        if (!ok[i]) continue;
+        l0[i] = p.lse_part[slot(0) + r0 + i];
+        l1[i] = p.lse_part[slot(1) + r0 + i];
+        v0[i] = load(slot(0) + r0 + i);
+        v1[i] = load(slot(1) + r0 + i);
+    }
+#pragma unroll
+    for (int i = 0; i < kPcWarpRows; ++i) {
+        if (!ok[i]) continue;
+        float M = fmaxf(l0[i], l1[i]);
+        float w0 = l0[i] == -INFINITY ? 0.0f : expf(l0[i] - M), w1 = l1[i] == -INFINITY ? 0.0f : expf(l1[i] - M);
+        float den = w0 + w1;
+        float4 acc = make_float4(w0 * v0[i].x + w1 * v1[i].x, w0 * v0[i].y + w1 * v1[i].y, w0 * v0[i].z + w1 * v1[i].z,
+                                 w0 * v0[i].w + w1 * v1[i].w);
 #pragma unroll 4
-        for (int x = 0; x < parts; ++x) {
-            const int64_t sl = slot(x);
-            const float lx = p.lse_part[sl];
-            const float w = lx == -INFINITY ? 0.0f : expf(lx - M);
-            const float4 v = *reinterpret_cast<const float4 *>(p.o_part + sl * kDv + 4 * lane);
-            den += w;
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
+        for (int x = 2; x < mg.parts; ++x) {
+            const float l = p.lse_part[slot(x) + r0 + i];
+            const float4 v = load(slot(x) + r0 + i);
+            const float top = fmaxf(M, l);
+            const float a = M == -INFINITY ? 0.0f : expf(M - top), w = l == -INFINITY ? 0.0f : expf(l - top);
+            M = top;
+            den = den * a + w;
+            acc = make_float4(acc.x * a + w * v.x, acc.y * a + w * v.y, acc.z * a + w * v.z, acc.w * a + w * v.w);
         }
+        const int in_tile = (r0 + i) % kPfRows, tok = (r0 + i) / kPfRows * p.tile_tokens + in_tile / p.G;
         const float inv = den > 0.0f ? 1.0f / den : 0.0f;
         const int64_t orow = (int64_t)(mg.row0 + tok) * p.heads + mg.g * p.G + in_tile % p.G;
         *reinterpret_cast<uint2 *>(p.out + orow * kDv + 4 * lane) =
