@@ -543,7 +543,8 @@ int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, cons
     if ((st = check_index(kv)) != GQLA_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
     if (total_q < 0 || num_splits == 0 || num_splits < -65535 || num_splits > 65535) return GQLA_ERR_INVALID_ARG;
-    if (!q || !q_starts || !kv_expanded || !k_rope || !out) return GQLA_ERR_INVALID_ARG;
+    // a list or a row tensor without entries may be NULL
+    if (!q_starts || !kv_expanded || !k_rope || (total_q > 0 && (!q || !out))) return GQLA_ERR_INVALID_ARG;
     const bool whole = num_splits <= 1;
     if (!whole && (!o_part || !lse_part)) return GQLA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kv_expanded) || !aligned16(k_rope) || !aligned16(out) ||
@@ -566,7 +567,7 @@ int gqla_append_cache(const gqla_dims *dims, const void *rows, int64_t total_q, 
     if (st != GQLA_OK) return st;
     if ((st = check_index(kv)) != GQLA_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
-    if (total_q < 0 || !rows || !q_starts) return GQLA_ERR_INVALID_ARG;
+    if (total_q < 0 || (total_q > 0 && !rows) || !q_starts) return GQLA_ERR_INVALID_ARG;
     // the expanded cache has two parts and takes both weights; at least one cache is written
     if ((kv_expanded == nullptr) != (k_rope == nullptr)) return GQLA_ERR_INVALID_ARG;
     if (kv_expanded ? (!w_uk || !w_uv) : !latent_cache) return GQLA_ERR_INVALID_ARG;
@@ -586,7 +587,7 @@ int gqla_copy_pages(const gqla_dims *dims, const int32_t *pairs, int64_t num_pai
     int st = check_ragged_dims(dims);
     if (st != GQLA_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
-    if (num_pairs < 0 || num_pages <= 0 || !pairs || !aligned8(pairs)) return GQLA_ERR_INVALID_ARG;
+    if (num_pairs < 0 || num_pages <= 0 || (num_pairs > 0 && !pairs) || !aligned8(pairs)) return GQLA_ERR_INVALID_ARG;
     if (!latent_cache && !kv_expanded && !k_rope) return GQLA_ERR_INVALID_ARG;
     if (!aligned16(latent_cache) || !aligned16(kv_expanded) || !aligned16(k_rope)) return GQLA_ERR_INVALID_ARG;
     if (num_pages > copy_pages_limit() || num_pairs > ((int64_t)1 << 31) - 1 || dims->num_groups > 4096)
@@ -601,7 +602,8 @@ int gqla_fork_sequences(const gqla_page_pool *pool, const int32_t *forks, int nu
     int st = check_pool(pool);
     if (st != GQLA_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
-    if (num_forks < 0 || !forks || !pairs || !aligned8(forks) || !aligned8(pairs)) return GQLA_ERR_INVALID_ARG;
+    if (num_forks < 0 || (num_forks > 0 && (!forks || !pairs)) || !aligned8(forks) || !aligned8(pairs))
+        return GQLA_ERR_INVALID_ARG;
     if (num_forks > 65535) return GQLA_ERR_UNSUPPORTED;
     if (num_forks == 0) return GQLA_OK;
     return cuda_status(launch_fork(pool, forks, num_forks, pairs, workspace, reinterpret_cast<cudaStream_t>(stream)));
@@ -621,7 +623,7 @@ int gqla_free_sequences(const gqla_page_pool *pool, const int32_t *seq_ids, int 
     int st = check_pool(pool);
     if (st != GQLA_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
-    if (num_ids < 0 || !seq_ids) return GQLA_ERR_INVALID_ARG;
+    if (num_ids < 0 || (num_ids > 0 && !seq_ids)) return GQLA_ERR_INVALID_ARG;
     if (num_ids > 65535) return GQLA_ERR_UNSUPPORTED;
     if (num_ids == 0) return GQLA_OK;
     return cuda_status(launch_free(pool, seq_ids, num_ids, workspace, reinterpret_cast<cudaStream_t>(stream)));

@@ -744,7 +744,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                             *reinterpret_cast<uint4 *>(dst[k] + at) =
                                 make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
                 };
-#pragma unroll 1
+#pragma unroll 2
                 for (int i = 0; i < kDv; i += 32) {
                     uint32_t r[32];
                     tmem_ld32(t_o + i, r);

@@ -90,3 +90,47 @@ def test_append_matches_the_projections(name, what):
     out, err = run(c, latent=what != "expanded", expanded=what != "latent")
     assert err[0] == 0
     check(c, out, latent=what != "expanded", expanded=what != "latent")
+
+
+def test_append_leaves_out_what_is_inconsistent_and_reports_it():
+    c = make(2, [20, 30, 40], [5, 100, 0], seed=3)
+    for bad, change in ((1, lambda d: d["seqlens"].__setitem__(1, 29)), (2, lambda d: d["seqlens"].__setitem__(2, 10 ** 6)),
+                        (0, lambda d: d["starts"].__setitem__(0, -1)), (2, lambda d: d["starts"].__setitem__(3, 91))):
+        d = dict(c, starts=c["starts"].clone(), seqlens=c["seqlens"].clone())
+        change(d)
+        out, err = run(d)
+        assert err == (-5, bad)
+        check(c, out, skip=(bad,))
+
+
+def test_append_skips_pages_outside_the_pool():
+    c = make(2, [20, 30], [5, 100], seed=4)
+    for page in (-1, c["pages"]):
+        d = dict(c, table=c["table"].clone())
+        d["table"][1, 2] = page  # tokens 128 and 129 of sequence 1
+        out, err = run(d)
+        assert err == (-5, 1)
+        e = dict(c, new=[20, 28], lens=[25, 128], row0=[0, 20, 48])
+        check(e, out)
+
+
+def test_append_far_offsets():
+    from decode_attention_06_b200 import gqla
+    c = make(1, [37, 5], [300, 60], seed=8)
+    pages = 140_000
+    far = dict(c, table=torch.where(c["table"] >= 0, c["table"] + (pages - c["pages"]), c["table"]), pages=pages)
+    kv = torch.zeros(1, pages * 64, 256, dtype=torch.bfloat16, device="cuda")
+    rope = torch.zeros(pages * 64, 64, dtype=torch.bfloat16, device="cuda")
+    latent = torch.zeros(pages, 64, 576, dtype=torch.bfloat16, device="cuda")
+    n = c["pages"]
+    kv.view(1, pages, 64, 256)[:, -n:] = c["kv"].view(1, n, 64, 256)
+    rope.view(pages, 64, 64)[-n:] = c["rope"].view(n, 64, 64)
+    latent[-n:] = c["latent"]
+    ws = gqla.new_workspace()
+    gqla.gqla_append_cache(gqla.make_dims(16, 1), c["rows"], c["starts"], gqla.make_kv_index(far["table"], c["seqlens"], pages),
+                           ws, latent_cache=latent, w_uk=c["w_uk"], w_uv=c["w_uv"], kv_expanded=kv, k_rope=rope)
+    torch.cuda.synchronize()
+    assert gqla.gqla_read_device_error(ws)[0] == 0
+    check(c, {"latent": latent[-n:], "kv": kv.view(1, pages, 64, 256)[:, -n:].reshape(1, n * 64, 256),
+              "rope": rope.view(pages, 64, 64)[-n:].reshape(n * 64, 64)})
+    assert not bool(kv.view(pages, -1)[:-n].any()) and not bool(latent[:-n].any())

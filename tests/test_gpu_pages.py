@@ -292,3 +292,95 @@ def test_pages_outside_the_pool_are_reported():
     g.free([3, 9, -1])
     g.error([1, 2])
     assert torch.equal(g.refs, refs)
+
+
+def test_copy_pages_far_offsets():
+    pages = 140_000
+    from decode_attention_06_b200 import gqla
+    kv = torch.zeros(1, pages * 64, 256, dtype=torch.bfloat16, device="cuda")
+    v = kv.view(pages, 64, 256)
+    v[3], v[pages - 2] = 3.0, 5.0
+    pairs = torch.tensor([[3, pages - 1], [pages - 2, 7]], dtype=torch.int32, device="cuda")
+    ws = gqla.new_workspace()
+    gqla.gqla_copy_pages(gqla.make_dims(16, 1), pairs, pages, ws, kv_expanded=kv)
+    torch.cuda.synchronize()
+    assert gqla.gqla_read_device_error(ws)[0] == 0
+    assert bool((v[pages - 1] == 3.0).all()) and bool((v[7] == 5.0).all()) and float(v.float().sum()) == 16.0 * 64 * 256
+
+
+def test_page_calls_in_a_graph():
+    """Fork, copy, extend and free captured once and replayed: each replay starts from the pool as it is."""
+    ref = Pool(4, 6, 30)
+    ref.extend([100, 64, 0, 0])
+    g = Gpu(ref)
+    forks, grow, gone = g.i32([[0, 2], [1, 3]]), g.i32([0, 0, 70, 1]), g.i32([2, 3])
+    pairs = torch.full((2, 2), 9, dtype=torch.int32, device="cuda")
+    kept = [x.clone() for x in (g.latent, g.kv, g.rope)]
+
+    def cycle():
+        g.gqla.gqla_fork_sequences(g.pool, forks, pairs, g.ws)
+        g.copy(pairs)
+        g.gqla.gqla_extend_sequences(g.pool, grow, g.ws)
+        g.gqla.gqla_free_sequences(g.pool, gone, g.ws)
+
+    cycle()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cycle()
+    exp, _ = ref.fork([(0, 2), (1, 3)])
+    want = copied(kept, 2, [p for p in exp if p[0] >= 0])
+    ref.extend([0, 0, 70, 1])
+    ref.free([2, 3])
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        g.same(ref)
+        assert pairs.tolist() == [list(p) for p in exp]
+        assert all(torch.equal(a, b) for a, b in zip((g.latent, g.kv, g.rope), want))
+    g.error([])
+
+
+def test_a_full_pool():
+    ref = Pool(4, 8, 5)
+    g = Gpu(ref)
+    for grow in ([130, 64, 65, 1], [0, 0, 0, 0], [62, 1, 0, 0]):
+        g.extend(grow)
+        bad = ref.extend(grow)
+        torch.cuda.synchronize()
+        g.same(ref)
+        g.error(bad)
+    pairs = g.fork([(0, 3)])
+    exp, bad = ref.fork([(0, 3)])
+    torch.cuda.synchronize()
+    assert pairs.tolist() == [list(p) for p in exp]
+    g.same(ref)
+    g.error(bad)
+
+
+def test_empty_calls():
+    ref = Pool(3, 4, 8)
+    g = Gpu(ref)
+    e = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    g.gqla.gqla_fork_sequences(g.pool, e, e.clone(), g.ws)
+    g.copy(e)
+    g.gqla.gqla_free_sequences(g.pool, torch.empty(0, dtype=torch.int32, device="cuda"), g.ws)
+    t, r, pairs, counts = g.compact(inplace=False)
+    torch.cuda.synchronize()
+    assert counts.tolist() == [0, 0] and pairs.tolist() == [[-1, -1]] * 4 and not bool(r.any())
+    g.same(ref)
+    g.error([])
+
+
+def test_one_page_pool():
+    ref = Pool(2, 1, 1)
+    g = Gpu(ref)
+    g.extend([64, 0])
+    ref.extend([64, 0])
+    g.fork([(0, 1)])
+    ref.fork([(0, 1)])
+    t, r, pairs, counts = g.compact()
+    torch.cuda.synchronize()
+    assert counts.tolist() == [1, 0] and pairs.tolist() == [[-1, -1]]
+    g.same(ref)
+    g.error([])

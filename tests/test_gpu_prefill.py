@@ -135,3 +135,166 @@ def test_prefill_matches_the_formula(name, splits):
     out, lse, err = call(c, splits)
     assert err[0] == 0
     check(c, out, lse)
+
+
+def test_prefill_without_lse_leaves_it_alone():
+    c = make(32, 8, [7, 40], [100, 3], seed=2)
+    out, lse, err = call(c, lse=False)
+    assert err[0] == 0 and bool((lse == 7.0).all())
+    want, _, tol, _ = reference(c)
+    assert bool(((out.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("factor", [4.0, 30.0])
+@pytest.mark.parametrize("splits", [None, -3, 11])
+def test_prefill_rising_scores(factor, splits):
+    """Keys that grow along the sequence: the running maximum rises by more than 2^8 tile after
+    tile, so O is rescaled all along (the decreasing order leaves every later tile negligible)."""
+    for flip in (False, True):
+        c = make(128, 8, [50, 3], [900, 1300], seed=9)
+        for b, L in enumerate(c["lens"]):
+            ramp = 1.0 + factor * torch.arange(L, device="cuda") / L
+            if flip:
+                ramp = ramp.flip(0)
+            sl = c["slots"][b]
+            c["rope"][sl] = (c["rope"][sl].float() * ramp[:, None]).to(torch.bfloat16)
+        out, lse, err = call(c, splits)
+        assert err[0] == 0
+        check(c, out, lse)
+
+
+def test_prefill_masked_keys_of_any_value():
+    """Keys and values that no row of a sequence sees hold NaN and infinities: tail slots, and the
+    pages of another sequence."""
+    for tail in (float("nan"), float("inf"), float("-inf"), torch.finfo(torch.bfloat16).min):
+        c = make(32, 8, [33, 1, 70], [95, 64, 57], seed=4, tail=tail)
+        out, lse, err = call(c)
+        assert err[0] == 0
+        check(c, out, lse)
+
+
+def test_prefill_later_tokens_do_not_reach_earlier_blocks():
+    """A NaN in a later token of the same sequence changes nothing for query blocks that end before it."""
+    c = make(128, 8, [200], [40], seed=5)
+    ref, ref_lse, _ = call(c, -5)
+    c["kv"][:, c["slots"][0][-9:]] = float("nan")  # blocks of 32 tokens: only the last two see or hold these
+    out, lse, err = call(c, -5)
+    assert err[0] == 0
+    assert torch.equal(out[:160], ref[:160]) and torch.equal(lse[:160], ref_lse[:160])
+
+
+def test_prefill_reports_inconsistent_sequences_and_finishes_the_rest():
+    c = make(32, 8, [20, 30, 40, 50], [5, 200, 0, 70], seed=6)
+    want, want_lse, tol, tol_l = reference(c)
+    for bad, change in ((1, lambda s, L: L.__setitem__(1, 29)), (3, lambda s, L: L.__setitem__(3, 10 ** 6)),
+                        (3, lambda s, L: s.__setitem__(4, 141)), (2, lambda s, L: L.__setitem__(2, -5))):
+        d = dict(c, starts=c["starts"].clone(), seqlens=c["seqlens"].clone())
+        change(d["starts"], d["seqlens"])
+        for splits in (None, 9):
+            out, lse, err = call(d, splits)
+            assert err == (-5, bad)
+            rows = slice(c["row0"][bad], c["row0"][bad + 1])
+            assert bool((out[rows] == 7.0).all()) and bool((lse[rows] == 7.0).all())
+            keep = torch.ones(out.shape[0], dtype=torch.bool, device="cuda")
+            keep[rows] = False
+            assert bool(((out[keep].double() - want[keep]).abs() <= tol[keep]).all())
+            assert bool(((lse[keep].double() - want_lse[keep]).abs() <= tol_l[keep]).all())
+
+
+def test_prefill_reports_pages_outside_the_pool():
+    c = make(32, 8, [20, 30, 40], [200, 200, 0], seed=7)
+    want, _, tol, _ = reference(c)
+    for page in (-1, c["pages"], 2 ** 31 - 1):
+        d = dict(c, table=c["table"].clone())
+        d["table"][1, 2] = page
+        out, _, err = call(d)
+        assert err == (-5, 1)
+        for b in (0, 2):
+            rows = slice(c["row0"][b], c["row0"][b + 1])
+            assert bool(((out[rows].double() - want[rows]).abs() <= tol[rows]).all())
+
+
+def test_prefill_far_offsets():
+    """Pages whose elements lie beyond 2^31 in the expanded cache."""
+    from decode_attention_06_b200 import gqla
+    pages = 140_000  # 140000 * 64 * 256 elements a group
+    c = make(16, 1, [37, 5], [300, 1000], seed=8)
+    move = torch.arange(pages - c["pages"], pages, device="cuda")
+    kv = torch.empty(1, pages * 64, 256, dtype=torch.bfloat16, device="cuda")
+    rope = torch.empty(pages * 64, 64, dtype=torch.bfloat16, device="cuda")
+    kv.view(1, pages, 64, 256)[:, move] = c["kv"].view(1, -1, 64, 256)
+    rope.view(pages, 64, 64)[move] = c["rope"].view(-1, 64, 64)
+    far = dict(c, table=torch.where(c["table"] >= 0, c["table"] + (pages - c["pages"]), c["table"]), kv=kv, rope=rope,
+               pages=pages)
+    out, lse, err = call(far)
+    assert err[0] == 0
+    check(c, out, lse)
+    del gqla
+
+
+def test_prefill_repeats_bit_for_bit():
+    c = make(128, 8, [300, 1, 17], [700, 3000, 0], seed=10)
+    ref = call(c, 29)
+    for _ in range(3):
+        out, lse, _ = call(c, 29)
+        assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_prefill_on_another_stream_and_in_a_graph():
+    from decode_attention_06_b200 import gqla
+    c = make(128, 8, [60, 9], [400, 1500], seed=11)
+    want, want_lse, tol, tol_l = reference(c)
+    side = torch.cuda.Stream()
+    out, lse, err = call(c, 21, stream=side)
+    assert err[0] == 0
+    check(c, out, lse)
+    # captured twice (divided and whole plans) into graphs that share the workspace and are replayed
+    # in turn, with new lengths and queries in place: the plan follows the device's numbers
+    dims = gqla.make_dims(c["h"], c["g"])
+    kv = gqla.make_kv_index(c["table"], c["seqlens"], c["pages"])
+    bufs = [gqla.PrefillBuffers(dims, c["q"].shape[0], s) for s in (21, -16)]
+    bufs[1].workspace = bufs[0].workspace
+    graphs = []
+    for b in bufs:
+        gqla.prefill_step(dims, b, c["q"], c["starts"], kv, c["kv"], c["rope"])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            gqla.prefill_step(dims, b, c["q"], c["starts"], kv, c["kv"], c["rope"])
+        graphs.append(g)
+    for new in ([60, 9], [31, 38], [1, 0], [69, 0]):
+        d = dict(c, new=new, lens=[400 + new[0], 1500 + new[1]], row0=[0, new[0], sum(new)])
+        if max(d["lens"][0] - c["lens"][0], d["lens"][1] - c["lens"][1]) > 0:
+            d["lens"] = [min(a, b) for a, b in zip(d["lens"], c["lens"])]
+        c["seqlens"].copy_(torch.tensor(d["lens"], dtype=torch.int32))
+        c["starts"].copy_(torch.tensor(d["row0"], dtype=torch.int32))
+        d["slots"] = [s[:n] for s, n in zip(c["slots"], d["lens"])]
+        c["q"].copy_(torch.randn_like(c["q"], dtype=torch.float32).to(torch.bfloat16))
+        for b, g in zip(bufs, graphs):
+            b.out.fill_(7.0)
+            b.lse.fill_(7.0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert gqla.gqla_read_device_error(b.workspace)[0] == 0
+            check(d, b.out, b.lse)
+
+
+def test_prefill_refuses_wrong_tensors():
+    from decode_attention_06_b200 import gqla
+    c = make(32, 8, [4], [3], seed=1)
+    dims = gqla.make_dims(32, 8)
+    kv = gqla.make_kv_index(c["table"], c["seqlens"], c["pages"])
+    b = gqla.PrefillBuffers(dims, 4, -8)
+    with pytest.raises(ValueError, match="contiguous"):
+        gqla.prefill_step(dims, b, c["q"].transpose(0, 1).contiguous().transpose(0, 1), c["starts"], kv, c["kv"], c["rope"])
+    with pytest.raises(ValueError, match="shape"):
+        gqla.prefill_step(dims, b, c["q"], c["starts"][:1], kv, c["kv"], c["rope"])
+    with pytest.raises(ValueError, match="bfloat16"):
+        gqla.prefill_step(dims, b, c["q"].float(), c["starts"], kv, c["kv"], c["rope"])
+    with pytest.raises(ValueError, match="CUDA"):
+        gqla.prefill_step(dims, b, c["q"].cpu(), c["starts"], kv, c["kv"], c["rope"])
+    with pytest.raises(ValueError, match="buffers hold"):
+        gqla.prefill_step(dims, gqla.PrefillBuffers(dims, 3, -8), c["q"], c["starts"], kv, c["kv"], c["rope"])
+    with pytest.raises(gqla.GqlaError) as e:
+        gqla.gqla_prefill_gqa(dims, c["q"], c["starts"], c["kv"], c["rope"], kv, 4, None, None, b.out, b.lse, b.workspace)
+    assert e.value.status == -1
