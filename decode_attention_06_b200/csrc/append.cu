@@ -287,11 +287,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
         st_cluster_b32(map_peer(smem_u32(const_cast<int *>(abort_flag)), rank ^ 1), 1);
     }
     cluster_sync();
-    if (*abort_flag) {
+    if (*abort_flag) {  // the same in both CTAs
         const long long t0 = clock64();
         while (clock64() - t0 < 200000) {}
+        cluster_sync();
     }
-    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);

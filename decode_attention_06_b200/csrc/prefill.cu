@@ -787,9 +787,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         if (!alive) *abort_flag = 1;
     }
 
-    // Leave together: a CTA that gave up tells the other one; after the first barrier none
-    // sends anything new, and if either gave up both wait until what is in flight (loads,
-    // commits: microseconds) has landed.
+    // Leave together: a CTA that gave up tells the other one; after the barrier none sends
+    // anything new, and if either gave up both wait until what is in flight (loads, commits:
+    // microseconds) has landed, and for each other once more.
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) {
@@ -797,11 +797,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         st_cluster_b32(map_peer(smem_u32(const_cast<int *>(abort_flag)), rank ^ 1), 1);
     }
     cluster_sync();
-    if (*abort_flag) {
+    if (*abort_flag) {  // the same in both CTAs
         const long long t0 = clock64();
         while (clock64() - t0 < 200000) {}
+        cluster_sync();
     }
-    cluster_sync();
     if (warp == 3) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);

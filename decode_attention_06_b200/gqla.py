@@ -325,138 +325,140 @@ def gqla_decode_gqa_noalloc(dims, q, kv_expanded, k_rope, kv, num_splits, out, l
 
 # ------------------------------------------------------------------ ragged batches of new tokens
 #
-# The calls from here on may be small (a step's tokens, a few pages), so their marshalling is kept
-# to what the checks need: _ptr instead of _dev, and the raw stream of the tensors' device. They
-# refuse tensors of another device than the current one.
+# The calls from here on may be small (a step's tokens, a few pages), so their marshalling does
+# no more than the checks need, and takes the raw stream of the current device. They refuse
+# tensors of another device than that.
 
-def _ptr(t, name, dtype, shape):
-    """Device address of a contiguous CUDA tensor of this type and shape on the current device."""
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _ptr(t, name, dtype, shape, dev):
+    """Device address of a contiguous tensor of this type and shape on device `dev`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != _current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _opt(t, name, dtype, shape):
-    return None if t is None else _ptr(t, name, dtype, shape)
+def _opt(t, name, dtype, shape, dev):
+    return None if t is None else _ptr(t, name, dtype, shape, dev)
 
 
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _raw(stream):
+def _raw(stream, dev):
     if stream is not None:
         return stream.cuda_stream
-    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(_current_device())
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(dev)
 
 
-def _ws(workspace):
+def _ws(workspace, dev):
     """(address, bytes) of a workspace."""
-    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    if workspace.get_device() != _current_device():
-        raise ValueError("workspace must be on the current device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
+    return workspace.data_ptr(), workspace.nbytes
 
 
-def _index_on_device(idx):
-    for t in idx._keep:
-        if t.get_device() != _current_device():
-            raise ValueError(f"the index is on {t.device}, the current device is cuda:{_current_device()}")
+def _here(idx, dev):
+    """An index or a pool, whose tensors must be on the current device."""
+    if idx._keep[0].get_device() != dev or idx._keep[-1].get_device() != dev:
+        raise ValueError(f"the index is on {idx._keep[0].device}, the current device is cuda:{dev}")
     return ctypes.byref(idx)
+
+
+def _prefill(dims, q, q_starts, kv_expanded, k_rope, kv, num_splits, dev, o_part, lse_part, out, lse, ws, stream):
+    """The call itself: inputs checked here, outputs and scratch given as addresses."""
+    n, total = kv.num_pages * kv.page_size, q.shape[0]
+    _check("gqla_prefill_gqa", _lib.gqla_prefill_gqa(
+        ctypes.byref(dims), _ptr(q, "q", _BF16, (total, dims.num_heads, D_QK), dev), total,
+        _ptr(q_starts, "q_starts", _I32, (kv.batch + 1,), dev),
+        _ptr(kv_expanded, "kv_expanded", _BF16, (dims.num_groups, n, D_NOPE + D_V), dev),
+        _ptr(k_rope, "k_rope", _BF16, (n, D_ROPE), dev), n, _here(kv, dev), num_splits,
+        o_part, lse_part, out, lse, *ws, _raw(stream, dev)))
 
 
 def gqla_prefill_gqa(dims, q, q_starts, kv_expanded, k_rope, kv, num_splits, o_part, lse_part, out, lse_out,
                      workspace, stream=None):
     """Attention of chunks of new tokens; o_part / lse_part are None for num_splits <= 1."""
-    n, h, total = kv.num_pages * kv.page_size, dims.num_heads, q.shape[0]
-    slots = gqla_prefill_slots(num_splits)
-    bf16, f32 = torch.bfloat16, torch.float32
-    ws, ws_bytes = _ws(workspace)
-    _check("gqla_prefill_gqa", _lib.gqla_prefill_gqa(
-        ctypes.byref(dims), _ptr(q, "q", bf16, (total, h, D_QK)), total,
-        _ptr(q_starts, "q_starts", torch.int32, (kv.batch + 1,)),
-        _ptr(kv_expanded, "kv_expanded", bf16, (dims.num_groups, n, D_NOPE + D_V)),
-        _ptr(k_rope, "k_rope", bf16, (n, D_ROPE)), n, _index_on_device(kv), num_splits,
-        _opt(o_part, "o_part", f32, (slots, PREFILL_BLOCK_ROWS, D_V)),
-        _opt(lse_part, "lse_part", f32, (slots, PREFILL_BLOCK_ROWS)),
-        _ptr(out, "out", bf16, (total, h, D_V)), _opt(lse_out, "lse_out", f32, (total, h)),
-        ws, ws_bytes, _raw(stream)))
+    dev, slots, rows = _current_device(), gqla_prefill_slots(num_splits), (q.shape[0], dims.num_heads)
+    _prefill(dims, q, q_starts, kv_expanded, k_rope, kv, num_splits, dev,
+             _opt(o_part, "o_part", _F32, (slots, PREFILL_BLOCK_ROWS, D_V), dev),
+             _opt(lse_part, "lse_part", _F32, (slots, PREFILL_BLOCK_ROWS), dev),
+             _ptr(out, "out", _BF16, (*rows, D_V), dev), _opt(lse_out, "lse_out", _F32, rows, dev),
+             _ws(workspace, dev), stream)
 
 
 def gqla_append_cache(dims, rows, q_starts, kv, workspace, latent_cache=None, w_uk=None, w_uv=None,
                       kv_expanded=None, k_rope=None, stream=None):
     """The latent rows of new tokens into the caches that are given (latent, expanded + RoPE keys)."""
-    n, total, g, bf16 = kv.num_pages * kv.page_size, rows.shape[0], dims.num_groups, torch.bfloat16
-    ws, ws_bytes = _ws(workspace)
+    dev, total, g = _current_device(), rows.shape[0], dims.num_groups
     _check("gqla_append_cache", _lib.gqla_append_cache(
-        ctypes.byref(dims), _ptr(rows, "rows", bf16, (total, D_ROW)), total,
-        _ptr(q_starts, "q_starts", torch.int32, (kv.batch + 1,)),
-        _opt(w_uk, "w_uk", bf16, (g, D_LATENT, D_NOPE)), _opt(w_uv, "w_uv", bf16, (g, D_LATENT, D_V)),
-        *_caches(dims, kv.num_pages, latent_cache, kv_expanded, k_rope), n, _index_on_device(kv),
-        ws, ws_bytes, _raw(stream)))
+        ctypes.byref(dims), _ptr(rows, "rows", _BF16, (total, D_ROW), dev), total,
+        _ptr(q_starts, "q_starts", _I32, (kv.batch + 1,), dev),
+        _opt(w_uk, "w_uk", _BF16, (g, D_LATENT, D_NOPE), dev), _opt(w_uv, "w_uv", _BF16, (g, D_LATENT, D_V), dev),
+        *_caches(dims, kv.num_pages, latent_cache, kv_expanded, k_rope, dev), kv.num_pages * kv.page_size,
+        _here(kv, dev), *_ws(workspace, dev), _raw(stream, dev)))
 
 
 # ------------------------------------------------------------------ the pages of a cache
 
-def _caches(dims, num_pages, latent_cache, kv_expanded, k_rope):
-    n, bf16 = num_pages * PAGE_SIZE, torch.bfloat16
-    return (_opt(latent_cache, "latent_cache", bf16, (num_pages, PAGE_SIZE, D_ROW)),
-            _opt(kv_expanded, "kv_expanded", bf16, (dims.num_groups, n, D_NOPE + D_V)),
-            _opt(k_rope, "k_rope", bf16, (n, D_ROPE)))
+def _caches(dims, num_pages, latent_cache, kv_expanded, k_rope, dev):
+    n = num_pages * PAGE_SIZE
+    return (_opt(latent_cache, "latent_cache", _BF16, (num_pages, PAGE_SIZE, D_ROW), dev),
+            _opt(kv_expanded, "kv_expanded", _BF16, (dims.num_groups, n, D_NOPE + D_V), dev),
+            _opt(k_rope, "k_rope", _BF16, (n, D_ROPE), dev))
 
 
 def gqla_copy_pages(dims, pairs, num_pages, workspace, latent_cache=None, kv_expanded=None, k_rope=None, stream=None):
     """Pages pairs[i] = (source, target) of the given caches; a negative source is skipped."""
-    ws, ws_bytes = _ws(workspace)
-    n = pairs.shape[0]
+    dev, n = _current_device(), pairs.shape[0]
     _check("gqla_copy_pages", _lib.gqla_copy_pages(
-        ctypes.byref(dims), _ptr(pairs, "pairs", torch.int32, (n, 2)), n, num_pages,
-        *_caches(dims, num_pages, latent_cache, kv_expanded, k_rope), ws, ws_bytes, _raw(stream)))
+        ctypes.byref(dims), _ptr(pairs, "pairs", _I32, (n, 2), dev), n, num_pages,
+        *_caches(dims, num_pages, latent_cache, kv_expanded, k_rope, dev), *_ws(workspace, dev), _raw(stream, dev)))
 
 
 def gqla_fork_sequences(pool, forks, pairs, workspace, stream=None):
     """forks[i] = (parent, child); pairs[i] receives the page copy that the fork needs, or (-1, -1)."""
-    ws, ws_bytes = _ws(workspace)
-    n = forks.shape[0]
+    dev, n = _current_device(), forks.shape[0]
     _check("gqla_fork_sequences", _lib.gqla_fork_sequences(
-        _index_on_device(pool), _ptr(forks, "forks", torch.int32, (n, 2)), n,
-        _ptr(pairs, "pairs", torch.int32, (n, 2)), ws, ws_bytes, _raw(stream)))
+        _here(pool, dev), _ptr(forks, "forks", _I32, (n, 2), dev), n, _ptr(pairs, "pairs", _I32, (n, 2), dev),
+        *_ws(workspace, dev), _raw(stream, dev)))
 
 
 def gqla_extend_sequences(pool, new_tokens, workspace, stream=None):
     """new_tokens[b] more tokens (and the pages for them) for every sequence."""
-    ws, ws_bytes = _ws(workspace)
+    dev = _current_device()
     _check("gqla_extend_sequences", _lib.gqla_extend_sequences(
-        _index_on_device(pool), _ptr(new_tokens, "new_tokens", torch.int32, (pool.batch,)), ws, ws_bytes, _raw(stream)))
+        _here(pool, dev), _ptr(new_tokens, "new_tokens", _I32, (pool.batch,), dev), *_ws(workspace, dev),
+        _raw(stream, dev)))
 
 
 def gqla_free_sequences(pool, seq_ids, workspace, stream=None):
     """The pages of the listed sequences lose one reference each; their lengths become 0."""
-    ws, ws_bytes = _ws(workspace)
-    n = seq_ids.shape[0]
+    dev, n = _current_device(), seq_ids.shape[0]
     _check("gqla_free_sequences", _lib.gqla_free_sequences(
-        _index_on_device(pool), _ptr(seq_ids, "seq_ids", torch.int32, (n,)), n, ws, ws_bytes, _raw(stream)))
+        _here(pool, dev), _ptr(seq_ids, "seq_ids", _I32, (n,), dev), n, *_ws(workspace, dev), _raw(stream, dev)))
 
 
 def gqla_compact_pages(pool, page_table_out, page_refs_out, pairs, counts, workspace, stream=None):
     """Live pages to the front; pairs receives the moves (gqla_copy_pages), counts = (live pages, moves).
     The outputs may be the pool's own tables."""
-    ws, ws_bytes = _ws(workspace)
-    i32 = torch.int32
+    dev, pages = _current_device(), pool.num_pages
     _check("gqla_compact_pages", _lib.gqla_compact_pages(
-        _index_on_device(pool), _ptr(page_table_out, "page_table_out", i32, (pool.batch, pool.max_pages_per_seq)),
-        _ptr(page_refs_out, "page_refs_out", i32, (pool.num_pages,)),
-        _ptr(pairs, "pairs", i32, (max(1, pool.num_pages // 2), 2)), _ptr(counts, "counts", i32, (2,)),
-        ws, ws_bytes, _raw(stream)))
+        _here(pool, dev), _ptr(page_table_out, "page_table_out", _I32, (pool.batch, pool.max_pages_per_seq), dev),
+        _ptr(page_refs_out, "page_refs_out", _I32, (pages,), dev),
+        _ptr(pairs, "pairs", _I32, (max(1, pages // 2), 2), dev), _ptr(counts, "counts", _I32, (2,), dev),
+        *_ws(workspace, dev), _raw(stream, dev)))
 
 
 # ------------------------------------------------------------------ helpers
@@ -627,15 +629,16 @@ class PrefillBuffers:
 def prefill_step(dims, bufs: PrefillBuffers, q, q_starts, kv, kv_expanded, k_rope, stream=None):
     """Attention of the new tokens q [total_q][h][192] through the C ABI.  Returns
     (out [total_q][h][128] bf16, lse [total_q][h])."""
-    total = q.shape[0]
-    if total > bufs.out.shape[0]:
-        raise ValueError(f"q has {total} tokens, the buffers hold {bufs.out.shape[0]}")
-    out, lse = bufs.out, bufs.lse
-    if total < out.shape[0]:
-        out, lse = out[:total], lse[:total]
-    gqla_prefill_gqa(dims, q, q_starts, kv_expanded, k_rope, kv, bufs.num_splits, bufs.o_part, bufs.lse_part,
-                     out, lse, bufs.workspace, stream)
-    return out, lse
+    total, out, lse, dev = q.shape[0], bufs.out, bufs.lse, _current_device()
+    if total > out.shape[0] or out.shape[1] != dims.num_heads or out.get_device() != dev:
+        raise ValueError(f"q has {total} tokens of {dims.num_heads} heads on cuda:{dev}, the buffers hold "
+                         f"{out.shape[0]} of {out.shape[1]} on {out.device}")
+    # the buffers are this module's own: types, sizes and layout are what the call wants
+    _prefill(dims, q, q_starts, kv_expanded, k_rope, kv, bufs.num_splits, dev,
+             None if bufs.o_part is None else bufs.o_part.data_ptr(),
+             None if bufs.lse_part is None else bufs.lse_part.data_ptr(), out.data_ptr(), lse.data_ptr(),
+             _ws(bufs.workspace, dev), stream)
+    return (out, lse) if total == out.shape[0] else (out[:total], lse[:total])
 
 
 class SparseBuffers:
