@@ -18,8 +18,8 @@
 //  * 12 warps: warp 0 TMA producer, warps 1 and 2 the issuers of S and of O, warp 3 TMEM owner
 //    and clears V rows past a block's last key; warps 4-7 and 8-11 the softmax of tile 0 and
 //    tile 1, one query row per thread (no exchange between threads), fp32 online softmax in the
-//    base-2 domain with lazy rescaling (O is touched only when a row's maximum rises by more
-//    than 2^8).
+//    base-2 domain, relative to a base that is set from a row's first tile and raised (O
+//    rescaled) only when a later one needs it.
 //  * K and V tiles pass through rings of three stages each.
 //  * Work split: prefill_plan.cuh. Every CTA derives its chunk from the device-resident
 //    lengths.
@@ -44,7 +44,8 @@ constexpr int kPfThreads = 384;
 constexpr int kPfLaunchRegs = 168;
 constexpr int kPfIssueRegs = 72, kPfSoftmaxRegs = 216;
 static_assert(128 * kPfIssueRegs + 256 * kPfSoftmaxRegs <= kPfThreads * kPfLaunchRegs, "register split");
-constexpr float kPfRescaleLog2 = 8.0f;
+constexpr float kPfRescaleLog2 = 8.0f;       // a base is raised when the maximum is 2^8 above it ...
+constexpr float kPfRise = 18446744073709551616.0f;  // ... or must be when a tile's sum is above 2^64
 
 constexpr int kPfBox = 64 * 128;          // one TMA box: 64 rows of 128 bytes
 constexpr int kPfK = 3 * kPfBox;          // a key tile's K in one CTA: its page's 64 keys x 192
@@ -285,39 +286,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-// Maximum that keeps a NaN.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // P = 2^(s scale - mu) of a row's 128 scores, rounded to bf16, into the row's P columns;
-// returns the sum of the unrounded values. FAST: also the largest score (NaN if one is).
-// (A share of the exponentials as polynomials on the FMA pipes does not pay here: the issue
-// slots and the power that they take cost more than the special-function unit's time. Step of
-// 128 keys: 3080 cycles without, 3190 with a quarter, 3610 with half.)
-template <bool FAST, typename Ready>
-__device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, float mu, uint32_t t_p, float &mx,
-                                        Ready ready) {
+// returns the sum of the unrounded values. (A share of the exponentials as polynomials on the
+// FMA pipes does not pay here: the issue slots and the power that they take cost more than the
+// special-function unit's time. Step of 128 keys: 3080 cycles without, 3190 with a quarter,
+// 3610 with half.)
+template <typename Ready>
+__device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, float mu, uint32_t t_p, Ready ready) {
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float2 sc = make_float2(scale, scale), sub = make_float2(-mu, -mu);
-    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < 128; i += 32) {
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-            const float2 s = make_float2(__uint_as_float(sv[i + e]), __uint_as_float(sv[i + e + 1]));
-            const float2 x = fma2(s, sc, sub);
+            const float2 x = fma2(make_float2(__uint_as_float(sv[i + e]), __uint_as_float(sv[i + e + 1])), sc, sub);
             const float2 v = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            if (FAST) top[(e >> 1) & 1] = max3_nan(top[(e >> 1) & 1], s.x, s.y);
             sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], v);
             __nv_bfloat162 h2 = __floats2bfloat162_rn(v.x, v.y);
             w[e / 2] = *reinterpret_cast<uint32_t *>(&h2);
@@ -325,7 +309,6 @@ __device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, 
         if (i == 0) ready();  // P of the step before has been used
         tmem_st16(t_p + i / 2, w);
     }
-    mx = max_nan(top[0], top[1]);
     const float2 t = add2(sum[0], sum[1]);
     return t.x + t.y;
 }
@@ -638,46 +621,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     // computed along and never stored)
                     const int lim = valid ? last + 1 - t * kPfTile : kPfTile;
                     const bool masked = __any_sync(0xffffffffu, lim < kPfTile);
-                    // P against the maximum so far, at once; only where a row's score rose more
-                    // than 2^8 above it (and on a piece's first tile, and under a mask) again
-                    // against the new one. A NaN score takes the second way.
-                    float lt = 0.0f;
-                    bool redo = t == t_first || masked;
-                    if (!redo) {
-                        float mx;
-                        lt = form_p<true>(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_p, mx, [&] { products(sn - 1); });
-                        redo = __any_sync(0xffffffffu, valid && !(mx * p.scale_log2 <= m + kPfRescaleLog2));
-                    }
-                    if (redo) {
-                        if (masked) {
+                    // P against the base so far, at once. The base of a row (its largest score when
+                    // it was set, in log2 units) need not be its maximum: bf16 and fp32 have the
+                    // exponents for P up to 2^64, and P, O and l are all relative to it. It
+                    // is set on a piece's first tile and under a mask, and again where a sum says
+                    // that the scores rose too far above it (or that there was none yet, or that
+                    // a score is NaN).
+                    float lt;
+                    for (bool fresh = t == t_first || masked;; fresh = true) {
+                        if (fresh) {
+                            if (masked) {
 #pragma unroll
-                            for (int e = 0; e < 128; ++e)
-                                if (e >= lim) sv[e] = 0xff800000u;
-                        }
-                        float mt = -INFINITY;
-#pragma unroll
-                        for (int e = 0; e < 128; e += 2)
-                            mt = fmaxf(mt, fmaxf(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])));
-                        mt *= p.scale_log2;
-                        const bool rise = mt > m + kPfRescaleLog2;
-                        const float a = rise ? fast_exp2(m - mt) : 1.0f;  // 0 from an empty row
-                        if (rise) m = mt;
-                        l *= a;
-                        products(sn - 1);
-                        if (t > t_first && __any_sync(0xffffffffu, rise)) {
-#pragma unroll 1
-                            for (int i = 0; i < kDv; i += 16) {
-                                uint32_t r[16];
-                                tmem_ld16(t_o + i, r);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * a);
-                                tmem_st16(t_o + i, r);
+                                for (int e = 0; e < 128; ++e)
+                                    if (e >= lim) sv[e] = 0xff800000u;
                             }
+                            float mt = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 128; e += 2)
+                                mt = fmaxf(mt, fmaxf(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])));
+                            mt *= p.scale_log2;
+                            const bool rise = mt > m + kPfRescaleLog2;
+                            const float a = rise ? fast_exp2(m - mt) : 1.0f;  // 0 from an empty row
+                            if (rise) m = mt;
+                            l *= a;
+                            products(sn - 1);
+                            if (t > t_first && __any_sync(0xffffffffu, rise)) {
+#pragma unroll 1
+                                for (int i = 0; i < kDv; i += 16) {
+                                    uint32_t r[16];
+                                    tmem_ld16(t_o + i, r);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * a);
+                                    tmem_st16(t_o + i, r);
+                                }
+                            }
+                            tmem_wait_st();
                         }
-                        tmem_wait_st();
-                        float mx;
-                        lt = form_p<false>(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_p, mx, [] {});
+                        lt = form_p(sv, p.scale_log2, m == -INFINITY ? 0.0f : m, t_p, [&] { products(sn - 1); });
+                        if (fresh || !__any_sync(0xffffffffu, valid && (m == -INFINITY || !(lt <= kPfRise)))) break;
                     }
                     l += lt;
                     tmem_wait_st();
