@@ -169,13 +169,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
         prefetch_tensormap(&wuk_map);
         prefetch_tensormap(&wuv_map);
     }
+    __syncwarp();
+    cluster_arrive();  // this thread's barriers are initialised
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
         tc_fence_before();
     }
     __syncthreads();
-    cluster_sync();
+    cluster_wait();  // the other CTA's are too
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();

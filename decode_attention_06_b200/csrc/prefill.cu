@@ -63,7 +63,7 @@ struct PfSmem {
     static constexpr int kNumBars = 5 * kPfStages + 4 + 2 + 1 + 2 + 2 + 2 + 1 + 2;
     static constexpr int kExchange = 2 * kPfRows * 4;              // m, l of the second half's rows
     static constexpr int oPlan = oBar + kNumBars * 8;              // PfPlan
-    static constexpr int oX = oPlan + 48;
+    static constexpr int oX = oPlan + 80;
     static constexpr int oMisc = oX + kExchange;                       // tmem base, abort flag
     static constexpr int kBytes = oMisc + 16;
     static constexpr int kAlloc = kBytes + 1024;
@@ -129,12 +129,13 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v) {
 struct PfPlan {
     int64_t u0, end, len;
     int b, g, i, t;
+    PfSeq s;  // sequence b
 };
 
 // One full warp: the plan of chunk c. Sequences with bad numbers are reported when `report`.
 __device__ PfPlan pf_plan(const PfParams &p, int c, bool report) {
     const int lane = threadIdx.x & 31;
-    PfPlan r{0, 0, 0, p.batch, 0, 0, 0};
+    PfPlan r{0, 0, 0, p.batch, 0, 0, 0, {0, 0, 0, false}};
     // the first 32 sequences stay in registers: a small batch is read once
     PfSeq s0{0, 0, 0, false};
     int64_t units0 = 0, total = 0;
@@ -167,6 +168,7 @@ __device__ PfPlan pf_plan(const PfParams &p, int c, bool report) {
             const int64_t per_group = __shfl_sync(0xffffffffu, mine, src) / p.groups;
             int64_t off = pos - start;
             r.b = b0 + src;
+            r.s = PfSeq{n, L, __shfl_sync(0xffffffffu, s.q0, src), false};
             r.g = (int)(off / per_group);
             off -= r.g * per_group;
             // the block that holds unit `off`: the last i with units_before(i) <= off
@@ -209,10 +211,8 @@ struct PfIter {
     int64_t u0, end;  // first unit of the next block, end of the chunk
     int b, g, i, t;
     bool started;
-    __device__ __forceinline__ PfIter(const PfParams &p, const PfPlan &plan)
-        : u0(plan.u0), end(plan.end), b(plan.b), g(plan.g), i(plan.i), t(plan.t), started(false) {
-        if (b < p.batch) s = pf_seq(p, b);
-    }
+    __device__ __forceinline__ explicit PfIter(const PfPlan &plan)
+        : s(plan.s), u0(plan.u0), end(plan.end), b(plan.b), g(plan.g), i(plan.i), t(plan.t), started(false) {}
     __device__ __forceinline__ bool next(const PfParams &p, PfPiece &o) {
         while (u0 < end) {
             if (started && (++i * 4 * p.tile_tokens >= s.n)) {
@@ -325,6 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     uint64_t *s_full = q_empty + 2, *s_free = s_full + 2, *p_full = s_free + 1, *pv_done = p_full + 2;
     uint64_t *o_free = pv_done + 2;
     uint64_t *x_full = o_free + 2, *v_part = x_full + 1, *drain = v_part + kPfStages;
+    static_assert(sizeof(PfPlan) <= SM::oX - SM::oPlan, "plan");
     PfPlan &plan = *reinterpret_cast<PfPlan *>(smem + SM::oPlan);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::oMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::oMisc + 4);
@@ -355,6 +356,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         prefetch_tensormap(&kr_map);
         prefetch_tensormap(&q_map);
     }
+    __syncwarp();
+    cluster_arrive();  // this thread's barriers are initialised
     if (warp == 3) {
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
@@ -367,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         if (lane == 0) plan = mine;
     }
     __syncthreads();
-    cluster_sync();  // the other CTA's barriers are initialised too
+    cluster_wait();  // the other CTA's barriers are initialised too
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -409,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     tma_load_3d_pair(dst + kPfBox, &kv_map, bar, kNope + 64 * (int)rank, sl.s1, g);
                     ++vn;
                 };
-                PfIter it(p, plan);
+                PfIter it(plan);
                 PfPiece pc;
                 Slots prev{0, 0};
                 int prev_g = -1;
@@ -463,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 const uint32_t hi = static_cast<uint32_t>(q_d >> 32), q_lo = static_cast<uint32_t>(q_d);
                 const uint32_t k_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + SM::oK), 16, 1024, kSw128));
                 uint32_t qn[2] = {0, 0}, sn = 0, s = 0;
-                PfIter it(p, plan);
+                PfIter it(plan);
                 PfPiece pc;
                 while (!*abort_flag && it.next(p, pc)) {
                     const int nq = pc.ntok > 2 * p.tile_tokens ? 2 : 1;
@@ -503,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 const uint64_t v_d = smem_desc(smem_u32(smem + SM::oV), 16, 1024, kSw128);  // V MN-major
                 const uint32_t hi = static_cast<uint32_t>(v_d >> 32), v_lo = static_cast<uint32_t>(v_d);
                 uint32_t pn[2] = {0, 0}, on[2] = {0, 0}, s = 0;
-                PfIter it(p, plan);
+                PfIter it(plan);
                 PfPiece pc;
                 while (!*abort_flag && it.next(p, pc)) {
                     const int nq = pc.ntok > 2 * p.tile_tokens ? 2 : 1;
@@ -540,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             // P = 0 in the product and are cleared so that 0 x NaN cannot enter it. V of such a
             // tile arrives on a barrier of this CTA, and this warp passes its bytes on to the
             // barrier that the O issuer waits for.
-            PfIter it(p, plan);
+            PfIter it(plan);
             PfPiece pc;
             PfMerge merge{0, 0, 0, 0};
             uint32_t s = 0, fixes = 0;
@@ -582,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         uint32_t xn = 0;
         const bool in_tile = row < p.tile_tokens * p.G;
         uint32_t sn = 0, pvn = 0;  // steps seen, and products of this tile known to be complete
-        PfIter it(p, plan);
+        PfIter it(plan);
         PfPiece pc;
         bool alive = true;  // the same in all lanes of the warp
         // the first n products of this tile are complete: P may be written, O changed or read

@@ -43,20 +43,25 @@ __host__ __device__ inline int64_t pf_chunk(int64_t total, int num_splits) {
     return k < 2 ? 2 : k;
 }
 
-// sum over i in [0, n) of floor((a i + b) / m): the lattice points under a line, by Euclid's
-// steps on (a, m). a n + b < 2^32.
-__host__ __device__ inline int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-    int64_t sum = 0;
+// sum over i in [0, n) of floor((a i + b) / 128): the lattice points under a line, by Euclid's
+// steps on (a, 128), the first of them with shifts. a n + b < 2^32.
+__host__ __device__ inline int64_t tile_sum(uint32_t n, uint32_t a, uint32_t b) {
+    static_assert(kPfTile == 128, "shifts");
+    int64_t sum = (int64_t)(a >> 7) * ((int64_t)n * (n - 1) / 2) + (int64_t)(b >> 7) * n;
+    uint32_t top = (a & 127) * n + (b & 127);
+    uint32_t m = a & 127;  // a and m trade places
+    a = 128;
+    if (top < 128) return sum;
+    n = top >> 7;
+    b = top & 127;
     while (true) {
-        if (a >= m) {
-            sum += (int64_t)(a / m) * ((int64_t)n * (n - 1) / 2);
-            a %= m;
-        }
+        sum += (int64_t)(a / m) * ((int64_t)n * (n - 1) / 2);
+        a %= m;
         if (b >= m) {
             sum += (int64_t)(b / m) * n;
             b %= m;
         }
-        const uint32_t top = a * n + b;
+        top = a * n + b;
         if (top < m) return sum;
         n = top / m;
         b = top % m;
@@ -72,7 +77,7 @@ __host__ __device__ inline int64_t pf_units_before(int n, int L, int T, int i) {
     const int W = 4 * T, full = n / W;
     const int f = i < full ? i : full;
     int64_t s = (int64_t)kPfBlockCost * i;
-    if (f > 0) s += 2 * floor_sum(f, kPfTile, W, (uint32_t)(L - n) + W + kPfTile - 1);
+    if (f > 0) s += 2 * tile_sum(f, W, (uint32_t)(L - n) + W + kPfTile - 1);
     if (i > full) s += (int64_t)pf_weight(n - full * W, T) * (((int64_t)L + kPfTile - 1) / kPfTile);
     return s;
 }

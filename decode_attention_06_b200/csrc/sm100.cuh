@@ -593,6 +593,14 @@ __device__ __forceinline__ void cluster_sync() {
                      : "memory");
 }
 
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // The arrive half of cluster_sync without its release ordering, for a CTA that
 // only lets the others go on (it may exit without the matching wait).
 __device__ __forceinline__ void cluster_arrive_relaxed() {
