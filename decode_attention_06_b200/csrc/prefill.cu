@@ -587,16 +587,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         uint32_t sn = 0, pvn = 0;  // steps seen, and products of this tile known to be complete
         PfIter it(plan);
         PfPiece pc;
-        bool alive = true;  // the same in all lanes of the warp
+        // A wait that runs out is not branched on (the turn-around of S would pay for the vote):
+        // it raises the abort flag, later waits return at once, and nothing is stored any more.
+        bool alive = true;
+        const uint32_t s_free_a = lead(s_free), p_full_a = lead(&p_full[q]);
         // the first n products of this tile are complete: P may be written, O changed or read
         auto products = [&](uint32_t n) {
             if (pvn < n) {
-                alive = __all_sync(0xffffffffu, mbar_wait(&pv_done[q], pvn & 1, abort_flag)) && alive;
+                alive &= mbar_wait(&pv_done[q], pvn & 1, abort_flag);
                 tc_fence_after();
                 ++pvn;
             }
         };
-        while (alive && it.next(p, pc)) {
+        while (it.next(p, pc)) {
             // a block of one MMA tile: both warpgroups take its rows, the even and the odd key
             // tiles, and the first joins the two at the end
             const bool one = pc.ntok <= 2 * p.tile_tokens, joined = one && pc.t1 - pc.t0 > 1;
@@ -609,8 +612,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             float m = -INFINITY, l = 0.0f;    // maximum (log2 units) and sum of this row
             const int t_first = pc.t0 + (one ? q : 0);
             for (int t = t_first; t < pc.t1; t += one ? 2 : 1) {
-                alive = __all_sync(0xffffffffu, mbar_wait_long(&s_full[q], sn++ & 1, abort_flag)) && alive;
-                if (!alive) break;
+                alive &= mbar_wait_long(&s_full[q], sn++ & 1, abort_flag);
+                if (!alive) *abort_flag = 1;
                 tc_fence_after();
                 if (warp_valid) {
                     uint32_t sv[128];
@@ -619,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote_relaxed(lead(s_free));
+                    if (lane == 0) mbar_arrive_remote_relaxed(s_free_a);
                     // keys of this tile that the row sees (rows of no token: whatever; they are
                     // computed along and never stored)
                     const int lim = valid ? last + 1 - t * kPfTile : kPfTile;
@@ -668,17 +671,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     tmem_wait_st();
                 } else {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote_relaxed(lead(s_free));
+                    if (lane == 0) mbar_arrive_remote_relaxed(s_free_a);
                     products(sn - 1);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote_relaxed(lead(&p_full[q]));
+                if (lane == 0) mbar_arrive_remote_relaxed(p_full_a);
             }
             // ---- epilogue: O / l and the LSE, to the output or to this piece's partial
-            if (alive) products(sn - 1);
-            if (alive) products(sn);
-            if (!alive) break;
+            products(sn - 1);
+            products(sn);
             if (joined && q == 1) {  // this half's O stays in TMEM, where the same lanes read it
                 xm[row] = m;
                 xl[row] = l;
@@ -689,8 +691,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             }
             float a0 = 1.0f, a1 = 0.0f;
             if (joined) {
-                alive = __all_sync(0xffffffffu, mbar_wait(x_full, xn++ & 1, abort_flag));
-                if (!alive) break;
+                alive &= mbar_wait(x_full, xn++ & 1, abort_flag);
                 tc_fence_after();
                 const float m1 = xm[row], top = fmaxf(m, m1);
                 a0 = m == -INFINITY ? 0.0f : fast_exp2(m - top);
@@ -705,7 +706,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             const int64_t prow = (int64_t)(2 * c + (pc.t0 == 0 ? 1 : 0)) * kPfBlockRows + part * kPfRows + row;
             const int64_t orow = (pc.row0 + tok) * p.heads + pc.g * p.G + hg;
             if (warp_valid) {
-                if (valid) {
+                if (valid && alive) {
                     if (!whole) p.lse_part[prow] = lse;
                     else if (p.lse_out) p.lse_out[orow] = lse;
                 }
@@ -717,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 char *dst[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(valid ? mine : nullptr),
+                    const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(valid && alive ? mine : nullptr),
                                                    (lane & ~3) + k);
                     dst[k] = a ? reinterpret_cast<char *>(a) + (lane & 3) * 16 : nullptr;
                 }
