@@ -412,13 +412,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     tma_load_3d_pair(dst + kPfBox, &kv_map, bar, kNope + 64 * (int)rank, sl.s1, g);
                     ++vn;
                 };
+                auto load_k = [&](int g, const Slots &sl) {
+                    const int st = stage(k_full, k_empty, kn, kPfK);
+                    if (st < 0) return;
+                    uint8_t *dst = smem + SM::oK + st * kPfK;  // K_nope, RoPE keys of this CTA's page
+                    const uint32_t bar = lead(&k_full[st]);
+                    const int y = rank ? sl.s1 : sl.s0;
+                    tma_load_3d_pair(dst, &kv_map, bar, 0, y, g);
+                    tma_load_3d_pair(dst + kPfBox, &kv_map, bar, 64, y, g);
+                    tma_load_2d_pair(dst + 2 * kPfBox, &kr_map, bar, 0, y);
+                    ++kn;
+                };
+                // Order: K of the next step before V of this one (whose stage frees later); at the
+                // end of a piece V, then the next piece's first K, and only then its queries, whose
+                // place frees last.
+                const uint32_t q_bytes = (uint32_t)(p.tile_tokens * p.G) * 128u;
                 PfIter it(plan);
                 PfPiece pc;
-                Slots prev{0, 0};
-                int prev_g = -1;
-                bool prev_last = false;
-                const uint32_t q_bytes = (uint32_t)(p.tile_tokens * p.G) * 128u;
                 while (!*abort_flag && it.next(p, pc)) {
+                    Slots sl = slots(pc, pc.t0);
+                    load_k(pc.g, sl);
                     for (int q = 0; q < 2 && 2 * q * p.tile_tokens < pc.ntok; ++q) {
                         if (!mbar_wait(&q_empty[q], (qn[q] & 1) ^ 1, abort_flag)) *abort_flag = 1;
                         if (*abort_flag) break;
@@ -429,23 +442,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                                              pc.g * p.G, (int)(pc.row0 + (2 * q + (int)rank) * p.tile_tokens));
                     }
                     for (int t = pc.t0; t < pc.t1 && !*abort_flag; ++t) {
-                        const Slots sl = slots(pc, t);
-                        const int y = rank ? sl.s1 : sl.s0;
-                        const int st = stage(k_full, k_empty, kn, kPfK);
-                        if (st < 0) break;
-                        uint8_t *dst = smem + SM::oK + st * kPfK;  // K_nope, RoPE keys of this CTA's page
-                        const uint32_t bar = lead(&k_full[st]);
-                        tma_load_3d_pair(dst, &kv_map, bar, 0, y, pc.g);
-                        tma_load_3d_pair(dst + kPfBox, &kv_map, bar, 64, y, pc.g);
-                        tma_load_2d_pair(dst + 2 * kPfBox, &kr_map, bar, 0, y);
-                        ++kn;
-                        if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev, prev_last);
-                        prev = sl;
-                        prev_g = pc.g;
-                        prev_last = t == pc.nt - 1 && pc.kv_end % kPfTile != 0;
+                        const Slots now = sl;
+                        if (t + 1 < pc.t1) {
+                            sl = slots(pc, t + 1);
+                            load_k(pc.g, sl);
+                        }
+                        if (!*abort_flag) load_v(pc.g, now, t == pc.nt - 1 && pc.kv_end % kPfTile != 0);
                     }
                 }
-                if (prev_g >= 0 && !*abort_flag) load_v(prev_g, prev, prev_last);
                 // every copy has been used, and the other CTA's commits have arrived here
                 auto drained = [&](uint64_t *emptyb, uint32_t n) {
                     for (uint32_t x = (n > kPfStages ? n - kPfStages : 0); x < n && !*abort_flag; ++x)
