@@ -139,6 +139,12 @@ def make_dims(num_heads: int, num_groups: int = 8, softmax_scale: Optional[float
                      1.0 / math.sqrt(D_NOPE + D_ROPE) if softmax_scale is None else softmax_scale)
 
 
+def _one_device(*tensors) -> int:
+    """The device index that the tensors share, -1 if they do not."""
+    devs = {t.get_device() for t in tensors}
+    return devs.pop() if len(devs) == 1 else -1
+
+
 def make_kv_index(page_table: torch.Tensor, seqlens: torch.Tensor, num_pages: int,
                   page_size: int = PAGE_SIZE):
     pt = _dev(page_table, "page_table", torch.int32)
@@ -147,6 +153,7 @@ def make_kv_index(page_table: torch.Tensor, seqlens: torch.Tensor, num_pages: in
         raise ValueError("page_table must be [batch][max_pages] and seqlens [batch]")
     idx = gqla_kv_index(pt, sl, page_table.shape[0], page_table.shape[1], page_size, num_pages)
     idx._keep = (page_table, seqlens)  # keep the tensors alive with the struct
+    idx._device = _one_device(page_table, seqlens)
     return idx
 
 
@@ -159,6 +166,7 @@ def make_page_pool(page_table: torch.Tensor, seqlens: torch.Tensor, page_refs: t
         raise ValueError("page_table must be [batch][max_pages], seqlens [batch] and page_refs [num_pages]")
     pool = gqla_page_pool(pt, sl, rf, page_table.shape[0], page_table.shape[1], page_size, page_refs.shape[0])
     pool._keep = (page_table, seqlens, page_refs)
+    pool._device = _one_device(page_table, seqlens, page_refs)
     return pool
 
 
@@ -366,12 +374,12 @@ def _ws(workspace, dev):
     """(address, bytes) of a workspace."""
     if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
-    return workspace.data_ptr(), workspace.nbytes
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _here(idx, dev):
     """An index or a pool, whose tensors must be on the current device."""
-    if idx._keep[0].get_device() != dev or idx._keep[-1].get_device() != dev:
+    if idx._device != dev:
         raise ValueError(f"the index is on {idx._keep[0].device}, the current device is cuda:{dev}")
     return ctypes.byref(idx)
 
