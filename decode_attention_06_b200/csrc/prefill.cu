@@ -95,6 +95,7 @@ struct PfParams {
     int64_t num_slots;
     int batch, max_pages, num_pages, num_splits, heads, groups, G, tile_tokens;
     bool whole;  // no block is divided: no partials, no merge
+    int drop_v;  // diagnostic: rank 0 never issues its V load of this step (-1: none)
     float scale_log2;
 };
 
@@ -416,6 +417,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 // V: both pages, this CTA's 64 columns
                 // (`last`: with rows past the block's keys, through warp 3)
                 auto load_v = [&](int g, const Slots &sl, bool last) {
+                    if (rank == 0 && (int)vn == p.drop_v) {
+                        ++vn;
+                        return;
+                    }
                     const int st = stage(v_full, v_empty, vn, kPfV);
                     if (st < 0) return;
                     uint8_t *dst = smem + SM::oV + st * kPfV;
@@ -870,6 +875,8 @@ __global__ void __launch_bounds__(32 * kPcWarps) prefill_combine_kernel(const Pf
 
 }  // namespace
 
+extern thread_local int g_drop_v_unit;  // set by gqla_debug_drop_v_load
+
 cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_starts, int heads, int num_groups,
                                const void *kv, const void *k_rope, int64_t num_slots, const gqla_kv_index *idx,
                                int num_splits, bool whole, float scale, float *o_part, float *lse_part, void *out,
@@ -891,6 +898,8 @@ cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_
     p.num_pages = idx->num_pages;
     p.num_splits = num_splits;
     p.whole = whole;
+    p.drop_v = g_drop_v_unit;
+    g_drop_v_unit = -1;
     p.heads = heads;
     p.groups = num_groups;
     p.G = G;

@@ -547,7 +547,8 @@ int gqla_clear_device_error(void *workspace, gqla_stream_t stream);
  * host thread leaves out one load -- gqla_decode_gqa (or
  * gqla_decode_gqa_noalloc): the V load of work unit `unit` (units count
  * (page pair, group) in issue order within a CTA); gqla_decode_absorb: the
- * latent load of tile `unit` (64-token tiles in issue order within a CTA) --
+ * latent load of tile `unit` (64-token tiles in issue order within a CTA);
+ * gqla_prefill_gqa: the V load of key tile `unit` (in issue order within a CTA) --
  * so the wait for it runs out after about two seconds: that call then
  * records GQLA_ERR_TIMEOUT in its workspace, its outputs are unspecified, and
  * the context stays usable.  -1 cancels.  Returns GQLA_OK, or

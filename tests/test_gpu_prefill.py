@@ -298,3 +298,17 @@ def test_prefill_refuses_wrong_tensors():
     with pytest.raises(gqla.GqlaError) as e:
         gqla.gqla_prefill_gqa(dims, c["q"], c["starts"], c["kv"], c["rope"], kv, 4, None, None, b.out, b.lse, b.workspace)
     assert e.value.status == -1
+
+
+@pytest.mark.parametrize("splits,unit", [(-8, 0), (5, 1)])
+def test_prefill_wait_that_runs_out_is_reported(splits, unit):
+    """A V load that never comes: the wait for it runs out after about two seconds, both CTAs of the pair
+    give up together, the call records GQLA_ERR_TIMEOUT, and the next call is correct."""
+    from decode_attention_06_b200 import gqla
+    c = make(32, 8, [40, 3], [300, 500], seed=12)
+    gqla.gqla_debug_drop_v_load(unit)
+    _, _, err = call(c, splits)
+    assert err[0] == -6
+    out, lse, err = call(c, splits)
+    assert err[0] == 0
+    check(c, out, lse)
