@@ -199,7 +199,7 @@ __device__ PfPlan pf_plan(const PfParams &p, int c, bool report) {
             r.u0 = pos - off;
             const int w = pf_weight(min(n - lo * 4 * T, 4 * T), T);
             // the first tile of the chunk (past the block's last one: the next block's)
-            r.t = p.whole ? (off > 0 ? INT_MAX : 0) : (int)((off + w - 1) / w);
+            r.t = p.whole ? (off > 0 ? INT_MAX : 0) : (int)((off + w - 1) >> (w - 1));
             return r;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
@@ -247,10 +247,10 @@ struct PfIter {
             o.ntok = min(4 * p.tile_tokens, s.n - first);
             o.pos0 = s.L - s.n + first;
             o.kv_end = o.pos0 + o.ntok;
-            o.nt = (o.kv_end + kPfTile - 1) / kPfTile;
+            o.nt = (int)((uint32_t)(o.kv_end + kPfTile - 1) / kPfTile);
             const int w = pf_weight(o.ntok, p.tile_tokens);
             o.t0 = t;
-            o.t1 = p.whole ? o.nt : (int)min((int64_t)o.nt, (end - u0 + w - 1) / w);
+            o.t1 = p.whole ? o.nt : (int)min((int64_t)o.nt, (end - u0 + w - 1) >> (w - 1));  // w is 1 or 2
             t = 0;
             u0 += (int64_t)w * o.nt + kPfBlockCost;
             if (o.t0 < o.t1) return true;
@@ -329,7 +329,8 @@ __device__ __forceinline__ float form_p(const uint32_t (&sv)[128], float scale, 
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     prefill_gqa_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap kr_map,
-                       const __grid_constant__ CUtensorMap q_map, const PfParams p) {
+                       const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap q_token_map,
+                       const PfParams p) {
     using SM = PfSmem;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -455,9 +456,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                         if (*abort_flag) break;
                         ++qn[q];
                         if (rank == 0) mbar_arrive_expect_tx(&q_full[q], 2 * 3 * q_bytes);
-                        for (int cb = 0; cb < 3; ++cb)  // rows past the batch read as zeros
-                            tma_load_3d_pair(smem + SM::oQ + (3 * q + cb) * kPfQBlock, &q_map, lead(&q_full[q]), 64 * cb,
-                                             pc.g * p.G, (int)(pc.row0 + (2 * q + (int)rank) * p.tile_tokens));
+                        // Tokens of this CTA's part. Where the block has none, zeros (tokens past the
+                        // batch): a product of zeros takes much less power than one of whatever
+                        // rows come next, and under the power limit that is time (G a multiple of
+                        // 8 rows, the swizzle's period; other G load what is there).
+                        const int first = (2 * q + (int)rank) * p.tile_tokens;
+                        const int here = min(max(pc.ntok - first, 0), p.tile_tokens);
+                        const uint32_t bar = lead(&q_full[q]);
+                        for (int cb = 0; cb < 3; ++cb) {
+                            uint8_t *dst = smem + SM::oQ + (3 * q + cb) * kPfQBlock;
+                            if (here == p.tile_tokens || p.G % 8 != 0) {
+                                tma_load_3d_pair(dst, &q_map, bar, 64 * cb, pc.g * p.G, (int)(pc.row0 + first));
+                            } else if (here == 0) {
+                                tma_load_3d_pair(dst, &q_map, bar, 64 * cb, pc.g * p.G, (int)p.total_q);
+                            } else {
+                                for (int i = 0; i < p.tile_tokens; ++i)
+                                    tma_load_3d_pair(dst + i * p.G * 128, &q_token_map, bar, 64 * cb, pc.g * p.G,
+                                                     i < here ? (int)(pc.row0 + first + i) : (int)p.total_q);
+                            }
+                        }
                     }
                     for (int t = pc.t0; t < pc.t1 && !*abort_flag; ++t) {
                         const Slots now = sl;
@@ -602,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         const int row = 32 * (warp & 3) + lane;    // this thread's query row: its TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t t_s = tmem + kPfColS + lane_off, t_p = tmem + p_col(q) + lane_off, t_o = tmem + o_col(q) + lane_off;
-        const int hg = row % p.G;                  // head of the group
+        const int row_tok = row / p.G, hg = row - row_tok * p.G;  // token of the part, head of the group
         float *const xm = reinterpret_cast<float *>(smem + SM::oX), *const xl = xm + kPfRows;
         uint32_t xn = 0;
         const bool in_tile = row < p.tile_tokens * p.G;
@@ -627,11 +644,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             const bool one = pc.ntok <= 2 * p.tile_tokens, joined = one && pc.t1 - pc.t0 > 1;
             if (one && q == 1 && !joined) continue;
             const int part = (one ? 0 : 2 * q) + (int)rank;        // 128-row part of the block
-            const int tok = part * p.tile_tokens + row / p.G;      // token of the block
+            const int tok = part * p.tile_tokens + row_tok;        // token of the block
             const bool valid = in_tile && tok < pc.ntok;
             const bool warp_valid = __any_sync(0xffffffffu, valid);
             const int last = pc.pos0 + tok;   // the last key this row sees
-            float m = -INFINITY, l = 0.0f;    // maximum (log2 units) and sum of this row
+            float m = valid ? -INFINITY : INFINITY, l = 0.0f;  // base (log2 units) and sum of this row
             const int t_first = pc.t0 + (one ? q : 0);
             for (int t = t_first; t < pc.t1; t += one ? 2 : 1) {
                 alive &= mbar_wait_long(&s_full[q], sn++ & 1, abort_flag);
@@ -645,8 +662,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_relaxed(s_free_a);
-                    // keys of this tile that the row sees (rows of no token: whatever; they are
-                    // computed along and never stored)
+                    // keys of this tile that the row sees (rows of no token are computed along, with
+                    // P = 0, and never stored)
                     const int lim = valid ? last + 1 - t * kPfTile : kPfTile;
                     const bool masked = __any_sync(0xffffffffu, lim < kPfTile);
                     // P against the base so far, at once. The base of a row (its largest score when
@@ -660,8 +677,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                         if (fresh) {
                             if (masked) {
 #pragma unroll
-                                for (int e = 0; e < 128; ++e)
-                                    if (e >= lim) sv[e] = 0xff800000u;
+                                for (int i = 0; i < 128; i += 32) {
+                                    if (!__any_sync(0xffffffffu, lim < i + 32)) continue;  // seen by all rows
+#pragma unroll
+                                    for (int e = i; e < i + 32; ++e)
+                                        if (e >= lim) sv[e] = 0xff800000u;
+                                }
                             }
                             float mt = -INFINITY;
 #pragma unroll
@@ -695,6 +716,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_relaxed(s_free_a);
                     products(sn - 1);
+                    if (t == t_first) {  // a warp without a token: P = 0, for the power that products of it save
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = 0;
+#pragma unroll
+                        for (int i = 0; i < 64; i += 16) tmem_st16(t_p + i, w);
+                        tmem_wait_st();
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -905,7 +934,7 @@ cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_
     p.G = G;
     p.tile_tokens = pf_tile_tokens(G);
     p.scale_log2 = scale * kLog2e;
-    CUtensorMap kvm, krm, qm;
+    CUtensorMap kvm, krm, qm, qtm;
     {
         const uint64_t dims[3] = {(uint64_t)kKv, (uint64_t)num_slots, (uint64_t)num_groups};
         const uint64_t strides[2] = {(uint64_t)kKv * 2, (uint64_t)num_slots * kKv * 2};
@@ -922,7 +951,10 @@ cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_
         const uint64_t dims[3] = {(uint64_t)kQk, (uint64_t)heads, (uint64_t)total_q};
         const uint64_t strides[2] = {(uint64_t)kQk * 2, (uint64_t)heads * kQk * 2};
         const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)p.tile_tokens};
-        if (!make_bf16_map(&qm, q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+        const uint32_t one[3] = {64, (uint32_t)G, 1};
+        if (!make_bf16_map(&qm, q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !make_bf16_map(&qtm, q, 3, dims, strides, one, CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
     }
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = once_per_device(ready, [] {
@@ -936,7 +968,8 @@ cudaError_t launch_prefill_gqa(const void *q, int64_t total_q, const int32_t *q_
                                                                                      : cudaSuccess;
     });
     if (e != cudaSuccess) return e;
-    e = launch_dependent(prefill_gqa_kernel, dim3(2 * num_splits), dim3(kPfThreads), PfSmem::kAlloc, stream, kvm, krm, qm, p);
+    e = launch_dependent(prefill_gqa_kernel, dim3(2 * num_splits), dim3(kPfThreads), PfSmem::kAlloc, stream, kvm, krm, qm,
+                         qtm, p);
     if (e != cudaSuccess || whole) return e;
     return launch_dependent(prefill_combine_kernel, dim3(num_splits - 1, kPfBlockRows / kPcRows),
                             dim3(32 * kPcWarps), 0, stream, p);
