@@ -3,19 +3,21 @@
 // shared RoPE key (GQLA, paperlayer.ai summary, sec. 3 "Two equivalent decoding paths": what
 // the one-shot expansion does to a whole cache, done to the tokens of one step or prompt).
 //
-//   D[256 rows x 256] = A[256 x 512] * B_g[512 x 256],  B_g = [W_UK_g | W_UV_g]
+//   D[256 rows x NC] = A[256 x 512] * B[512 x NC],  B = [W_UK_g | W_UV_g] (NC = 256) or one of
+//   the two (NC = 128)
 //
-// A CTA pair (cta_group::2) takes 256 rows and a share of the groups: each CTA holds its 128
-// rows of A (K-major, 128 KB) for all of them and streams one half of B_g (rank 0 W_UK_g,
-// rank 1 W_UV_g; MN-major, the weights as stored) through a ring of 64-row slabs, so that
-// the weights cross from L2 once per 256 rows; two 256-column TMEM accumulators let the
-// epilogue of group g run during the products of g + 1. The cache slot of a row follows from
-// q_starts, the lengths and the page table; the threads look theirs up while the operands are
-// on their way. Two warps copy the latent rows and the RoPE keys.
+// A CTA pair (cta_group::2) takes 256 rows and a share of the products: each CTA holds its 128
+// rows of A (K-major, 128 KB) for all of them and streams one half of B's columns (MN-major,
+// the weights as stored) through a ring of 64-row slabs, so that the weights cross from L2
+// once per 256 rows; two TMEM accumulators let the epilogue of one product run during the
+// next. The cache slot of a row follows from q_starts, the lengths and the page table; the
+// threads look theirs up while the operands are on their way. Two warps copy the latent rows
+// and the RoPE keys.
 //
 // Bound by the tensor cores for many rows (2.1 MFLOP a row at 8 groups against 6.5 KB) and by
-// latency for a step's rows: 8190 rows 20.7 us (790 TFLOP/s, 2.55 TB/s: four groups a pair in one
-// wave, 9 us of MMA, the rest the first operands' way in and the last group's out), 128 rows 9.4.
+// latency for a step's rows: 7752 rows 20.4 us (798 TFLOP/s, 2.6 TB/s: four groups a pair in one
+// wave, 9 us of MMA, the rest the launch, the first operands' way in and the last group's out),
+// 128 rows 7.5 us.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -35,23 +37,24 @@ constexpr int kApBoxA = kApRows * 128;     // [128 rows][64 latent columns]
 constexpr int kApA = 8 * kApBoxA;
 constexpr int kApSlab = 64;                // K rows of B per ring stage
 constexpr int kApBoxB = kApSlab * 128;     // [64 K rows][64 columns]
-constexpr int kApStage = 2 * kApBoxB;      // one CTA's 128 columns
 constexpr int kApStages = 4;
 constexpr int kApSlabs = kLatent / kApSlab;
 constexpr int kApCopyRows = 16;            // rows copied at a time by the two copying warps
 constexpr int kApCopyBytes = kApCopyRows / 2 * kRow * 2;  // one warp's
 
+template <int NC>
 struct ApSmem {
+    static constexpr int kStage = NC / 128 * kApBoxB;  // one CTA's NC / 2 columns
     static constexpr int oA = 0;
     static constexpr int oB = oA + kApA;
-    static constexpr int oCopy = oB + kApStages * kApStage;
+    static constexpr int oCopy = oB + kApStages * kStage;
     static constexpr int oBar = oCopy + 2 * kApCopyBytes;
     // a_full[8], b_full/b_empty[kApStages], acc_full/acc_empty[2], drain, copy[2]
     static constexpr int kNumBars = 8 + 2 * kApStages + 4 + 1 + 2;
     static constexpr int oMisc = oBar + kNumBars * 8;
     static constexpr int kAlloc = oMisc + 16 + 1024;
 };
-static_assert(ApSmem::kAlloc <= 227 * 1024, "shared memory");
+static_assert(ApSmem<256>::kAlloc <= 227 * 1024, "shared memory");
 
 struct ApParams {
     const uint4 *rows;            // [total][576] bf16
@@ -62,7 +65,7 @@ struct ApParams {
     void *ws;
     int64_t total, num_slots;
     int batch, max_pages, num_pages;
-    int groups;                   // groups of one pair
+    int products;                 // products (of NC columns) of one pair
 };
 
 // Cache slot of row r, or -1 if it belongs to no (valid) sequence or its page is outside the
@@ -141,10 +144,11 @@ __global__ void __launch_bounds__(64) append_latent_kernel(const ApParams p) {
     if (threadIdx.x == 0 && abort_flag) report_error(p.ws, GQLA_ERR_TIMEOUT, (int)blockIdx.x);
 }
 
+template <int NC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
     append_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant__ CUtensorMap wuk_map,
                   const __grid_constant__ CUtensorMap wuv_map, const ApParams p) {
-    using SM = ApSmem;
+    using SM = ApSmem<NC>;
     constexpr int ST = kApStages;
     const int64_t row0 = (int64_t)blockIdx.x * kApRows;
     extern __shared__ uint8_t smem_raw[];
@@ -156,7 +160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::oMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int g0 = blockIdx.y * p.groups;  // this pair's first group
+    const int first = blockIdx.y * p.products;  // this pair's first product
     // the barriers that the MMA issuer waits for are those of rank 0
     auto lead = [](uint64_t *bar) { return map_peer(smem_u32(bar), 0); };
 
@@ -190,23 +194,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
         if (elect_one()) {
-            const CUtensorMap *w_map = rank ? &wuv_map : &wuk_map;
             int u = 0;
-            for (int x = 0; x < p.groups && !*abort_flag; ++x)
+            for (int x = 0; x < p.products && !*abort_flag; ++x) {
+                // this CTA's columns: of W_UK_g or W_UV_g, all 128 (NC = 256) or 64 of them
+                const int v = first + x, g = v * NC / kKv;
+                const CUtensorMap *w_map = (NC == 256 ? (int)rank : v & 1) ? &wuv_map : &wuk_map;
                 for (int kb = 0; kb < kApSlabs; ++kb, ++u) {
-                    if (x == 0) {  // a box of A with each slab of the first group
+                    if (x == 0) {  // a box of A with each slab of the first product
                         if (rank == 0) mbar_arrive_expect_tx(&a_full[kb], 2 * kApBoxA);
                         tma_load_2d_pair(smem + SM::oA + kb * kApBoxA, &row_map, lead(&a_full[kb]), 64 * kb, (int)row0);
                     }
                     const int st = u % ST;
                     if (!mbar_wait(&b_empty[st], ((u / ST) & 1) ^ 1, abort_flag)) *abort_flag = 1;
                     if (*abort_flag) break;
-                    uint8_t *dst = smem + SM::oB + st * kApStage;
-                    if (rank == 0) mbar_arrive_expect_tx(&b_full[st], 2 * kApStage);
-                    const int y = (g0 + x) * kLatent + kb * kApSlab;
-                    tma_load_2d_pair(dst, w_map, lead(&b_full[st]), 0, y);
-                    tma_load_2d_pair(dst + kApBoxB, w_map, lead(&b_full[st]), 64, y);
+                    uint8_t *dst = smem + SM::oB + st * SM::kStage;
+                    if (rank == 0) mbar_arrive_expect_tx(&b_full[st], 2 * SM::kStage);
+                    const int y = g * kLatent + kb * kApSlab;
+                    if (NC == 256) {
+                        tma_load_2d_pair(dst, w_map, lead(&b_full[st]), 0, y);
+                        tma_load_2d_pair(dst + kApBoxB, w_map, lead(&b_full[st]), 64, y);
+                    } else {
+                        tma_load_2d_pair(dst, w_map, lead(&b_full[st]), 64 * (int)rank, y);
+                    }
                 }
+            }
             // every copy has been used, and the other CTA's commits have arrived here
             for (int i = u > ST ? u - ST : 0; i < u && !*abort_flag; ++i)
                 if (!mbar_wait(&b_empty[i % ST], (i / ST) & 1, abort_flag)) *abort_flag = 1;
@@ -214,13 +225,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (rank == 0 && elect_one()) {
-            constexpr uint32_t idesc = idesc_bf16(2 * kApRows, 256, 0, 1);
-            // A K-major, 64-column boxes; B MN-major, two atoms of 64 columns in each CTA
+            constexpr uint32_t idesc = idesc_bf16(2 * kApRows, NC, 0, 1);
+            // A K-major, 64-column boxes; B MN-major, atoms of 64 columns
             const uint64_t a_d = smem_desc(smem_u32(smem + SM::oA), kApBoxB, 1024, kSw128);
             const uint32_t b_lo0 = static_cast<uint32_t>(smem_desc(smem_u32(smem + SM::oB), kApBoxB, 1024, kSw128));
             const uint32_t a_lo = static_cast<uint32_t>(a_d), hi = static_cast<uint32_t>(a_d >> 32);
             int u = 0;
-            for (int x = 0; x < p.groups && !*abort_flag; ++x) {
+            for (int x = 0; x < p.products && !*abort_flag; ++x) {
                 const int ab = x & 1;
                 if (!mbar_wait(&acc_empty[ab], ((x >> 1) & 1) ^ 1, abort_flag)) *abort_flag = 1;
                 for (int kb = 0; kb < kApSlabs; ++kb, ++u) {
@@ -229,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
                     ok = ok && mbar_wait(&b_full[st], (u / ST) & 1, abort_flag);
                     if (!ok) *abort_flag = 1;
                     tc_fence_after();
-                    const uint32_t a = a_lo + (kb * kApBoxA >> 4), b = b_lo0 + (st * kApStage >> 4);
+                    const uint32_t a = a_lo + (kb * kApBoxA >> 4), b = b_lo0 + (st * SM::kStage >> 4);
 #pragma unroll
                     for (int ks = 0; ks < kApSlab / 16; ++ks)
                         mma_bf16_pair(tmem + 256 * ab, a + (ks * 32 >> 4), b + (ks * 2048 >> 4), hi, idesc,
@@ -244,8 +255,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- epilogue
-        // two warps to a TMEM lane quadrant, one for K_nope's columns and one for V's
-        const int quad = warp & 3, col0 = (warp - 4) >> 2 ? kNope : 0;
+        // two warps to a TMEM lane quadrant, one for each half of the columns
+        const int quad = warp & 3, col0 = (warp - 4) >> 2 ? NC / 2 : 0;
         const int64_t r = row0 + 32 * quad + lane;
         const uint32_t lane_off = static_cast<uint32_t>(32 * quad) << 16;
         const int64_t slot = r < p.total ? ap_slot(p, r, false) : -1;
@@ -253,22 +264,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
         int64_t to[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, slot, (lane & ~3) + k);
-        for (int x = 0; x < p.groups; ++x) {
+        for (int x = 0; x < p.products; ++x) {
             const int ab = x & 1;
             if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ab], (x >> 1) & 1, abort_flag))) {
                 *abort_flag = 1;
                 break;
             }
             tc_fence_after();
-            __nv_bfloat16 *base = p.kv + (int64_t)(g0 + x) * p.num_slots * kKv + (lane & 3) * 8;
+            const int v = first + x;
+            __nv_bfloat16 *base = p.kv + (int64_t)(v * NC / kKv) * p.num_slots * kKv + v * NC % kKv + (lane & 3) * 8;
 #pragma unroll 2
-            for (int cc = col0; cc < col0 + kNope; cc += 32) {
-                uint32_t v[32], w[16];
-                tmem_ld32(tmem + 256 * ab + lane_off + cc, v);
+            for (int cc = col0; cc < col0 + NC / 2; cc += 32) {
+                uint32_t o[32], w[16];
+                tmem_ld32(tmem + 256 * ab + lane_off + cc, o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
                     w[i] = *reinterpret_cast<uint32_t *>(&t);
                 }
                 quad_transpose(w, lane);
@@ -304,6 +316,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
     }
 }
 
+template <int NC>
+cudaError_t launch_append_nc(const CUtensorMap &rm, const CUtensorMap &wuk, const CUtensorMap &wuv, const ApParams &p,
+                             dim3 grid, cudaStream_t stream) {
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = once_per_device(ready, [] {
+        return cudaFuncSetAttribute(append_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, ApSmem<NC>::kAlloc);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_dependent(append_kernel<NC>, grid, dim3(kApThreads), ApSmem<NC>::kAlloc, stream, rm, wuk, wuv, p);
+}
+
 }  // namespace
 
 cudaError_t launch_append(const void *rows, int64_t total, const int32_t *q_starts, const void *w_uk,
@@ -323,7 +346,7 @@ cudaError_t launch_append(const void *rows, int64_t total, const int32_t *q_star
     p.batch = idx->batch;
     p.max_pages = idx->max_pages_per_seq;
     p.num_pages = idx->num_pages;
-    p.groups = 0;
+    p.products = 0;
     const unsigned tiles = (unsigned)((total + kApRows - 1) / kApRows);
     if (!kv) return launch_dependent(append_latent_kernel, dim3(tiles, 8), dim3(64), 0, stream, p);
     CUtensorMap rm, wuk, wuv;
@@ -343,19 +366,19 @@ cudaError_t launch_append(const void *rows, int64_t total, const int32_t *q_star
     }
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // the groups over as many pairs as one wave holds: few rows read the weights' 2 MB through
-    // many SMs
+    // The products over as many pairs as one wave holds. Few rows: half a group's columns to a
+    // pair, so that the weights' 2 MB come in through as many SMs as there are (128 rows: 9.2 us
+    // with a group to a pair, 7.5 us so); many: whole groups, N = 256, which reads A from shared
+    // memory half as often.
     const int64_t pairs = (tiles + 1) / 2;
+    if (pairs * 2 * num_groups <= sms / 2) {
+        p.products = 1;
+        return launch_append_nc<128>(rm, wuk, wuv, p, dim3((unsigned)(2 * pairs), 2 * num_groups), stream);
+    }
     int split = 1;
     while (split * 2 <= num_groups && num_groups % (split * 2) == 0 && pairs * split * 2 <= sms / 2) split *= 2;
-    p.groups = num_groups / split;
-    static std::atomic<uint64_t> ready{0};
-    const cudaError_t e = once_per_device(ready, [] {
-        return cudaFuncSetAttribute(append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ApSmem::kAlloc);
-    });
-    if (e != cudaSuccess) return e;
-    return launch_dependent(append_kernel, dim3((unsigned)(2 * pairs), split), dim3(kApThreads), ApSmem::kAlloc, stream,
-                            rm, wuk, wuv, p);
+    p.products = num_groups / split;
+    return launch_append_nc<256>(rm, wuk, wuv, p, dim3((unsigned)(2 * pairs), split), stream);
 }
 
 }  // namespace gqla
