@@ -75,7 +75,8 @@ struct PfSmem {
     static constexpr int kNumBars = 5 * kPfStages + 4 + 2 + 1 + 2 + 2 + 2 + 1 + 2;
     static constexpr int kExchange = 2 * kPfRows * 4;              // m, l of the second half's rows
     static constexpr int oPlan = oBar + kNumBars * 8;              // PfPlan
-    static constexpr int oX = oPlan + 80;
+    static constexpr int oList = oPlan + 48;                       // PfListed[kPfListed]
+    static constexpr int oX = oList + 128 * 16;
     static constexpr int oMisc = oX + kExchange;                       // tmem base, abort flag
     static constexpr int kBytes = oMisc + 16;
     static constexpr int kAlloc = kBytes + 1024;
@@ -137,74 +138,98 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v) {
     return v;
 }
 
-// A pair's chunk: units [start of block (b, g, i), end) from tile t of that block on; `len`
-// is the length of every chunk. Nothing to do if b is past the batch.
+// A pair's chunk: units [start of block (g, i) of its first sequence, end) from tile t of that
+// block on; `len` is the length of every chunk. Its sequences, those without new tokens left out,
+// are listed in shared memory (the first kPfListed of them; the iterator reads on from there).
+constexpr int kPfListed = 128;
 struct PfPlan {
     int64_t u0, end, len;
-    int b, g, i, t;
-    PfSeq s;  // sequence b
+    int listed, g, i, t;
+};
+struct PfListed {
+    int b, n, L, q0;
 };
 
-// One full warp: the plan of chunk c. Sequences with bad numbers are reported when `report`.
-__device__ PfPlan pf_plan(const PfParams &p, int c, bool report) {
-    const int lane = threadIdx.x & 31;
-    PfPlan r{0, 0, 0, p.batch, 0, 0, 0, {0, 0, 0, false}};
-    // the first 32 sequences stay in registers: a small batch is read once
+// The whole CTA: the plan of chunk c. Sequences with bad numbers are reported when `report`.
+__device__ void pf_plan(const PfParams &p, int c, bool report, PfPlan *plan, PfListed *list) {
+    constexpr int kWarps = kPfThreads / 32;
+    __shared__ int64_t sums[kWarps], first_start;
+    __shared__ int counts[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the first sequence of a thread stays in registers: a batch of up to 384 is read once
     PfSeq s0{0, 0, 0, false};
     int64_t units0 = 0, total = 0;
-    for (int b = lane; b < p.batch; b += 32) {
+    for (int b = threadIdx.x; b < p.batch; b += kPfThreads) {
         const PfSeq s = pf_seq(p, b);
         if (s.bad && report) report_error(p.ws, GQLA_ERR_DEVICE, b);
         const int64_t u = pf_seq_units(p, s);
         total += u;
-        if (b < 32) { s0 = s; units0 = u; }
+        if (b < kPfThreads) { s0 = s; units0 = u; }
     }
     total = warp_sum64(total);
-    r.len = pf_chunk(total, p.num_splits);
-    const int64_t pos = c * r.len;
-    if (pos >= total) return r;
-    r.end = min(total, pos + r.len);
+    if (lane == 0) sums[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kWarps; ++w) total += sums[w];
+    const int64_t len = pf_chunk(total, p.num_splits), pos = c * len, end = min(total, pos + len);
     int64_t base = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const int b = b0 + lane;
+    int taken = 0;
+    for (int b0 = 0; b0 < p.batch && base < end; b0 += kPfThreads) {
+        const int b = b0 + threadIdx.x;
         PfSeq s{0, 0, 0, false};
         int64_t mine = 0;
         if (b0 == 0) { s = s0; mine = units0; }
         else if (b < p.batch) { s = pf_seq(p, b); mine = pf_seq_units(p, s); }
         const int64_t incl = warp_scan64(mine);
-        const unsigned hit = __ballot_sync(0xffffffffu, mine > 0 && base + incl > pos);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            const int64_t start = base + __shfl_sync(0xffffffffu, incl - mine, src);
-            const int n = __shfl_sync(0xffffffffu, s.n, src), L = __shfl_sync(0xffffffffu, s.L, src);
-            const int T = p.tile_tokens, m = pf_blocks(n, T);
-            const int64_t per_group = __shfl_sync(0xffffffffu, mine, src) / p.groups;
-            int64_t off = pos - start;
-            r.b = b0 + src;
-            r.s = PfSeq{n, L, __shfl_sync(0xffffffffu, s.q0, src), false};
-            r.g = (int)(off / per_group);
-            off -= r.g * per_group;
-            // the block that holds unit `off`: the last i with units_before(i) <= off
-            int lo = 0, hi = m;
-            while (hi - lo > 1) {
-                const int step = (hi - lo + 31) / 32;
-                const int at = lo + (lane + 1) * step;
-                const bool le = at < hi && pf_units_before(n, L, T, at) <= off;
-                const int k = __popc(__ballot_sync(0xffffffffu, le));
-                hi = min(hi, lo + (k + 1) * step);
-                lo += k * step;
-            }
-            r.i = lo;
-            off -= pf_units_before(n, L, T, lo);
-            r.u0 = pos - off;
-            const int w = pf_weight(min(n - lo * 4 * T, 4 * T), T);
-            // the first tile of the chunk (past the block's last one: the next block's)
-            r.t = p.whole ? (off > 0 ? INT_MAX : 0) : (int)((off + w - 1) >> (w - 1));
-            return r;
+        __syncthreads();
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        int64_t start = base + incl - mine;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) start += sums[w];
+            base += sums[w];
         }
-        base += __shfl_sync(0xffffffffu, incl, 31);
+        // the sequences that the chunk meets, in order
+        const bool in = mine > 0 && start < end && start + mine > pos;
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (lane == 0) counts[warp] = __popc(m);
+        __syncthreads();
+        int at = taken + __popc(m & ((1u << lane) - 1));
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) at += counts[w];
+            taken += counts[w];
+        }
+        if (in && at == 0) first_start = start;
+        if (in && at < kPfListed) list[at] = PfListed{b, s.n, s.L, (int)s.q0};
     }
-    return r;
+    __syncthreads();
+    if (warp != 0) return;
+    PfPlan r{0, 0, len, min(taken, kPfListed), 0, 0, 0};
+    if (taken > 0) {
+        r.end = end;
+        const int n = list[0].n, L = list[0].L, T = p.tile_tokens, blocks = pf_blocks(n, T);
+        const int64_t per_group = pf_units_before(n, L, T, blocks);
+        int64_t off = pos - first_start;
+        r.g = (int)(off / per_group);
+        off -= r.g * per_group;
+        // the block that holds unit `off`: the last i with units_before(i) <= off
+        int lo = 0, hi = blocks;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int at = lo + (lane + 1) * step;
+            const bool le = at < hi && pf_units_before(n, L, T, at) <= off;
+            const int k = __popc(__ballot_sync(0xffffffffu, le));
+            hi = min(hi, lo + (k + 1) * step);
+            lo += k * step;
+        }
+        r.i = lo;
+        off -= pf_units_before(n, L, T, lo);
+        r.u0 = pos - off;
+        const int w = pf_weight(min(n - lo * 4 * T, 4 * T), T);
+        // the first tile of the chunk (past the block's last one: the next block's)
+        r.t = p.whole ? (off > 0 ? INT_MAX : 0) : (int)((off + w - 1) >> (w - 1));
+    }
+    if (lane == 0) *plan = r;
 }
 
 // One piece: key tiles [t0, t1) of a query block.
@@ -220,32 +245,56 @@ struct PfPiece {
 
 // Walks the pieces of a chunk; the same in every role.
 struct PfIter {
-    PfSeq s;
+    const PfListed *list;
     int64_t u0, end;  // first unit of the next block, end of the chunk
-    int b, g, i, t;
+    int64_t q0;       // the sequence's first query row
+    int listed, at;   // sequences in the list, the place of this one (counted on past the list)
+    int b, n, L;      // the sequence
+    int g, i, t;
     bool started;
-    __device__ __forceinline__ explicit PfIter(const PfPlan &plan)
-        : s(plan.s), u0(plan.u0), end(plan.end), b(plan.b), g(plan.g), i(plan.i), t(plan.t), started(false) {}
+    __device__ __forceinline__ PfIter(const PfPlan &plan, const PfListed *seqs)
+        : list(seqs), u0(plan.u0), end(plan.end), listed(plan.listed), at(0), g(plan.g), i(plan.i), t(plan.t),
+          started(false) {
+        if (listed > 0) take(list[0]);
+    }
+    __device__ __forceinline__ void take(const PfListed &s) {
+        b = s.b;
+        n = s.n;
+        L = s.L;
+        q0 = s.q0;
+    }
+    // False past the batch.
+    __device__ __forceinline__ bool next_sequence(const PfParams &p) {
+        if (++at < listed) {
+            take(list[at]);
+            return true;
+        }
+        while (++b < p.batch) {
+            const PfSeq s = pf_seq(p, b);
+            n = s.n;
+            L = s.L;
+            q0 = s.q0;
+            if (n > 0) return true;
+        }
+        return false;
+    }
     __device__ __forceinline__ bool next(const PfParams &p, PfPiece &o) {
         while (u0 < end) {
-            if (started && (++i * 4 * p.tile_tokens >= s.n)) {
+            if (started && ++i * 4 * p.tile_tokens >= n) {
                 i = 0;
                 if (++g == p.groups) {
                     g = 0;
-                    do {
-                        ++b;
-                        if (b < p.batch) s = pf_seq(p, b);
-                    } while (b < p.batch && s.n == 0);
+                    if (!next_sequence(p)) end = u0;
+                    if (u0 >= end) return false;
                 }
             }
             started = true;
-            if (b >= p.batch) return false;
             const int first = i * 4 * p.tile_tokens;
             o.b = b;
             o.g = g;
-            o.row0 = s.q0 + first;
-            o.ntok = min(4 * p.tile_tokens, s.n - first);
-            o.pos0 = s.L - s.n + first;
+            o.row0 = q0 + first;
+            o.ntok = min(4 * p.tile_tokens, n - first);
+            o.pos0 = L - n + first;
             o.kv_end = o.pos0 + o.ntok;
             o.nt = (int)((uint32_t)(o.kv_end + kPfTile - 1) / kPfTile);
             const int w = pf_weight(o.ntok, p.tile_tokens);
@@ -340,8 +389,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     uint64_t *s_full = q_empty + 2, *s_free = s_full + 2, *p_full = s_free + 1, *pv_done = p_full + 2;
     uint64_t *o_free = pv_done + 2;
     uint64_t *x_full = o_free + 2, *v_part = x_full + 1, *drain = v_part + kPfStages;
-    static_assert(sizeof(PfPlan) <= SM::oX - SM::oPlan, "plan");
+    static_assert(sizeof(PfPlan) <= SM::oList - SM::oPlan && kPfListed * sizeof(PfListed) <= SM::oX - SM::oList, "plan");
     PfPlan &plan = *reinterpret_cast<PfPlan *>(smem + SM::oPlan);
+    PfListed *const list = reinterpret_cast<PfListed *>(smem + SM::oList);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::oMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::oMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -380,10 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
     }
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 0) {
-        const PfPlan mine = pf_plan(p, c, blockIdx.x == 0);
-        if (lane == 0) plan = mine;
-    }
+    pf_plan(p, c, blockIdx.x == 0, &plan, list);
     __syncthreads();
     cluster_wait();  // the other CTA's barriers are initialised too
     tc_fence_after();
@@ -446,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 // end of a piece V, then the next piece's first K, and only then its queries, whose
                 // place frees last.
                 const uint32_t q_bytes = (uint32_t)(p.tile_tokens * p.G) * 128u;
-                PfIter it(plan);
+                PfIter it(plan, list);
                 PfPiece pc;
                 while (!*abort_flag && it.next(p, pc)) {
                     Slots sl = slots(pc, pc.t0);
@@ -505,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 const uint32_t hi = static_cast<uint32_t>(q_d >> 32), q_lo = static_cast<uint32_t>(q_d);
                 const uint32_t k_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + SM::oK), 16, 1024, kSw128));
                 uint32_t qn[2] = {0, 0}, sn = 0, s = 0;
-                PfIter it(plan);
+                PfIter it(plan, list);
                 PfPiece pc;
                 while (!*abort_flag && it.next(p, pc)) {
                     const int nq = pc.ntok > 2 * p.tile_tokens ? 2 : 1;
@@ -545,7 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 const uint64_t v_d = smem_desc(smem_u32(smem + SM::oV), 16, 1024, kSw128);  // V MN-major
                 const uint32_t hi = static_cast<uint32_t>(v_d >> 32), v_lo = static_cast<uint32_t>(v_d);
                 uint32_t pn[2] = {0, 0}, on[2] = {0, 0}, s = 0;
-                PfIter it(plan);
+                PfIter it(plan, list);
                 PfPiece pc;
                 while (!*abort_flag && it.next(p, pc)) {
                     const int nq = pc.ntok > 2 * p.tile_tokens ? 2 : 1;
@@ -582,7 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             // P = 0 in the product and are cleared so that 0 x NaN cannot enter it. V of such a
             // tile arrives on a barrier of this CTA, and this warp passes its bytes on to the
             // barrier that the O issuer waits for.
-            PfIter it(plan);
+            PfIter it(plan, list);
             PfPiece pc;
             PfMerge merge{0, 0, 0, 0};
             uint32_t s = 0, fixes = 0;
@@ -624,7 +671,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
         uint32_t xn = 0;
         const bool in_tile = row < p.tile_tokens * p.G;
         uint32_t sn = 0, pvn = 0;  // steps seen, and products of this tile known to be complete
-        PfIter it(plan);
+        PfIter it(plan, list);
         PfPiece pc;
         // A wait that runs out is not branched on (the turn-around of S would pay for the vote):
         // it raises the abort flag, later waits return at once, and nothing is stored any more.

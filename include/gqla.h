@@ -327,7 +327,9 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
  * n_b > L_b, L_b beyond its page-table row) is reported (GQLA_ERR_DEVICE, info = b)
  * and its rows are left as they were; a page index outside the pool is reported the
  * same way and leaves that sequence's rows unspecified.  Cached rows past L_b may hold
- * anything, NaN too.
+ * anything, NaN too, and so may keys that a query does not see; values (V) of the L_b
+ * tokens are finite (one that is not reaches all rows of its query block of 4 (128 / G)
+ * tokens, G = h/g, those before it too).
  * Precision: bf16 operands, scores, softmax and its sum in fp32, P rounded to bf16
  * (the tensor-core operand), O accumulated in fp32, one rounding to bf16.
  */

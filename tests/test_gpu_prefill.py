@@ -312,3 +312,15 @@ def test_prefill_wait_that_runs_out_is_reported(splits, unit):
     out, lse, err = call(c, splits)
     assert err[0] == 0
     check(c, out, lse)
+
+
+@pytest.mark.parametrize("batch,every,n", [(900, 1, 1), (1500, 400, 30), (1000, 7, 3)])
+@pytest.mark.parametrize("splits", [None, 1, -9])
+def test_prefill_large_batches(batch, every, n, splits):
+    """More sequences than a CTA has threads, most of them without new tokens; more in a chunk than
+    its list holds."""
+    new = [n if b % every == 0 else 0 for b in range(batch)]
+    c = make(16, 2, new, [(b * 37) % 150 for b in range(batch)], seed=13)
+    out, lse, err = call(c, splits)
+    assert err[0] == 0
+    check(c, out, lse)
