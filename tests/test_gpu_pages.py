@@ -384,3 +384,21 @@ def test_one_page_pool():
     assert counts.tolist() == [1, 0] and pairs.tolist() == [[-1, -1]]
     g.same(ref)
     g.error([])
+
+
+def test_extend_by_more_pages_than_32_bits_count():
+    from decode_attention_06_b200 import gqla
+    batch, width, pages = 66, 1 << 25, 8  # every row may hold 2^31 tokens
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    table = torch.empty(batch, width, dtype=torch.int32, device="cuda")
+    table[:, :pages] = -7
+    lens, refs, ws = i32([0] * batch), i32([0] * pages), gqla.new_workspace()
+    pool = gqla.make_page_pool(table, lens, refs)
+    most = (1 << 31) - 1
+    gqla.gqla_extend_sequences(pool, i32([100] + [most] * (batch - 1)), ws)
+    torch.cuda.synchronize()
+    assert lens.tolist() == [100] + [0] * (batch - 1)
+    assert refs.tolist() == [1, 1] + [0] * (pages - 2)
+    assert table[0, :pages].tolist() == [0, 1] + [-7] * (pages - 2) and bool((table[1:, :pages] == -7).all())
+    st, info = gqla.gqla_read_device_error(ws)
+    assert st == -5 and 1 <= info < batch
