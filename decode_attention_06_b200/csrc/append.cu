@@ -68,17 +68,31 @@ struct ApParams {
     int products;                 // products (of NC columns) of one pair
 };
 
-// Cache slot of row r, or -1 if it belongs to no (valid) sequence or its page is outside the
-// pool (reported when `report`): the last b with q_starts[b] <= r, by bisection.
-__device__ int64_t ap_slot(const ApParams &p, int64_t r, bool report) {
+// Cache slot of row r (of no row where !has), or -1 if it belongs to no (valid) sequence or its
+// page is outside the pool (reported when `report`). By the whole warp: each lane bisects for
+// the last b with q_starts[b] <= r; rows that this leaves without a sequence are looked for in
+// all of them if the starts do not ascend (then a valid sequence may lie beside the bad ones).
+__device__ int64_t ap_slot(const ApParams &p, int64_t r, bool has, bool report) {
     int lo = 0, hi = p.batch;  // q_starts[lo] <= r < q_starts[hi], where they ascend
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (p.q_starts[mid] <= r) lo = mid;
         else hi = mid;
     }
-    const RaggedSeq s = ragged_seq(p.q_starts, p.seqlens, lo, p.total, p.max_pages);
-    if (r < s.q0 || r >= s.q0 + s.n) return -1;
+    auto owns = [&](const RaggedSeq &s) { return r >= s.q0 && r < s.q0 + s.n; };
+    RaggedSeq s = ragged_seq(p.q_starts, p.seqlens, lo, p.total, p.max_pages);
+    bool found = owns(s);
+    if (__any_sync(0xffffffffu, has && !found)) {
+        bool falls = false;
+        for (int b = threadIdx.x & 31; b < p.batch; b += 32) falls |= p.q_starts[b + 1] < p.q_starts[b];
+        if (__any_sync(0xffffffffu, falls))
+            for (int b = 0; b < p.batch && has && !found; ++b) {
+                s = ragged_seq(p.q_starts, p.seqlens, lo = b, p.total, p.max_pages);
+                found = owns(s);
+            }
+        __syncwarp();
+    }
+    if (!has || !found) return -1;
     const int t = s.L - s.n + (int)(r - s.q0);
     const int page = p.page_table[(int64_t)lo * p.max_pages + t / kPage];
     if (page < 0 || page >= p.num_pages) {
@@ -107,7 +121,7 @@ __device__ __forceinline__ void ap_copy(const ApParams &p, int64_t row0, int w, 
             mbar_arrive_expect_tx(bar, rows * kRowBytes);
             bulk_load(stage, reinterpret_cast<const uint8_t *>(p.rows) + r * kRowBytes, rows * kRowBytes, bar);
         }
-        const int64_t s = lane < rows ? ap_slot(p, r + lane, true) : -1;
+        const int64_t s = ap_slot(p, r + lane, lane < rows, true);
         if (!__all_sync(0xffffffffu, mbar_wait(bar, n & 1, abort_flag))) {
             *abort_flag = 1;
             break;
@@ -259,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kApThreads, 1)
         const int quad = warp & 3, col0 = (warp - 4) >> 2 ? NC / 2 : 0;
         const int64_t r = row0 + 32 * quad + lane;
         const uint32_t lane_off = static_cast<uint32_t>(32 * quad) << 16;
-        const int64_t slot = r < p.total ? ap_slot(p, r, false) : -1;
+        const int64_t slot = ap_slot(p, r, r < p.total, false);
         // four lanes trade 16-byte units, so that they write 64 bytes of one row together
         int64_t to[4];
 #pragma unroll

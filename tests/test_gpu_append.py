@@ -134,3 +134,14 @@ def test_append_far_offsets():
     check(c, {"latent": latent[-n:], "kv": kv.view(1, pages, 64, 256)[:, -n:].reshape(1, n * 64, 256),
               "rope": rope.view(pages, 64, 64)[-n:].reshape(n * 64, 64)})
     assert not bool(kv.view(pages, -1)[:-n].any()) and not bool(latent[:-n].any())
+
+
+@pytest.mark.parametrize("at,value,skip", [(1, 95, (0, 1)), (2, 10, (1, 2)), (1, -3, (0, 1))])
+def test_append_does_the_sequences_beside_starts_that_descend(at, value, skip):
+    c = make(2, [20, 30, 40], [5, 100, 0], seed=5)  # starts 0, 20, 50, 90
+    d = dict(c, starts=c["starts"].clone())
+    d["starts"][at] = value
+    for what in (dict(), dict(expanded=False)):
+        out, err = run(d, **what)
+        assert err[0] == -5 and err[1] in skip
+        check(c, out, skip=skip, **what)
