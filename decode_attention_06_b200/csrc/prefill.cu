@@ -797,8 +797,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 l = l * a0 + xl[row] * a1;
                 m = top;
             }
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            const float lse = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            // l = 0: no key seen. A NaN among the scores makes l, and so the row and its LSE, NaN
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            const float lse = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
             const float w0 = a0 * inv, w1 = a1 * inv;
             const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
             const int64_t prow = (int64_t)(2 * c + (pc.t0 == 0 ? 1 : 0)) * kPfBlockRows + part * kPfRows + row;
@@ -941,11 +942,11 @@ __global__ void __launch_bounds__(32 * kPcWarps) prefill_combine_kernel(const Pf
             acc = make_float4(acc.x * a + w * v.x, acc.y * a + w * v.y, acc.z * a + w * v.z, acc.w * a + w * v.w);
         }
         const int in_tile = (r0 + i) % kPfRows, tok = (r0 + i) / kPfRows * p.tile_tokens + in_tile / p.G;
-        const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+        const float inv = den != 0.0f ? 1.0f / den : 0.0f;
         const int64_t orow = (int64_t)(mg.row0 + tok) * p.heads + mg.g * p.G + in_tile % p.G;
         *reinterpret_cast<uint2 *>(p.out + orow * kDv + 4 * lane) =
             pack_bf16x4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (lane == 0 && p.lse_out) p.lse_out[orow] = den > 0.0f ? M + logf(den) : -INFINITY;
+        if (lane == 0 && p.lse_out) p.lse_out[orow] = den != 0.0f ? M + logf(den) : -INFINITY;
     }
 }
 

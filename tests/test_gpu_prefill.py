@@ -324,3 +324,34 @@ def test_prefill_large_batches(batch, every, n, splits):
     out, lse, err = call(c, splits)
     assert err[0] == 0
     check(c, out, lse)
+
+
+@pytest.mark.parametrize("shape", ["verify", "tile_edge", "heads4", "heads12", "g4_heads32"])
+@pytest.mark.parametrize("splits", [None, 7, -3])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_prefill_nan_scores_reach_their_rows_only(shape, splits, what):
+    """A query row that holds NaN or infinity and a key that does: NaN in the rows that see them, in
+    out and in the LSE, and the formula everywhere else."""
+    h, g, new, ctx = SHAPES[shape]
+    c = make(h, g, new, ctx, seed=8, gap=2)
+    b = len(new) - 1  # the key: the last sequence's second new token's, of group 0
+    c["kv"][0, c["slots"][b][ctx[b] + 1], 7] = what
+    c["q"][c["row0"][0], 1, 5] = what
+    c["q"][c["row0"][0], 1, 9] = -what  # with infinities the scores differ in sign, or are NaN
+    nan = torch.zeros(c["q"].shape[0], h, dtype=torch.bool, device="cuda")
+    nan[c["row0"][0], 1] = True
+    nan[c["row0"][b] + 1:c["row0"][b + 1], :h // g] = True
+    if what == math.inf:  # an infinite score of either sign is right or NaN, as the formula is
+        clean = dict(c, kv=c["kv"].clone(), q=c["q"].clone())
+        clean["kv"][0, c["slots"][b][ctx[b] + 1], 7] = 0
+        clean["q"][c["row0"][0], 1, [5, 9]] = 0
+    else:
+        clean = dict(c, kv=c["kv"].nan_to_num(0.0), q=c["q"].nan_to_num(0.0))
+    out, z, tol_o, tol_l = reference(clean)
+    got, lse, err = call(c, splits)
+    assert err[0] == 0
+    if what != math.inf:
+        assert bool(torch.isnan(got[nan]).all()) and bool(torch.isnan(lse[nan]).all())
+    keep = ~nan & ~torch.isnan(z)
+    assert bool(((got.double() - out).abs() <= tol_o)[keep].all())
+    assert bool(((lse.double() - z).abs() <= tol_l)[keep].all())
