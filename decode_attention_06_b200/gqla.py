@@ -592,8 +592,8 @@ def gqla_version() -> int:
 
 def gqla_debug_drop_v_load(unit: int):
     """Diagnostic: the next decode or prefill call of this thread leaves out one load
-    (GQA decode, prefill: a V load; absorb decode: a latent tile), so its bounded wait runs out and the call
-    records GQLA_ERR_TIMEOUT (-1 cancels)."""
+    (GQA decode, prefill: a V load; absorb decode: a latent tile), so its bounded wait runs
+    out and the call records GQLA_ERR_TIMEOUT (-1 cancels)."""
     _check("gqla_debug_drop_v_load", _lib.gqla_debug_drop_v_load(unit))
 
 
