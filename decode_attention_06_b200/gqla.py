@@ -620,7 +620,8 @@ class DecodeBuffers:
 
 
 class PrefillBuffers:
-    """Device buffers of gqla_prefill_gqa for up to total_q new tokens at one split count."""
+    """Device buffers of gqla_prefill_gqa for up to total_q new tokens at one split count;
+    calls that may run at the same time each need their own."""
 
     def __init__(self, dims, total_q: int, num_splits: int, device="cuda"):
         h, slots = dims.num_heads, gqla_prefill_slots(num_splits)

@@ -318,7 +318,8 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
  *                block is divided, one kernel, no partials
  *   o_part       fp32 [gqla_prefill_slots(C)][512][128], lse_part fp32
  *                [gqla_prefill_slots(C)][512]: the partials; 16-byte aligned; NULL when
- *                num_splits <= 1
+ *                num_splits <= 1.  Calls that may run at the same time (two streams,
+ *                two graphs) each need their own
  *   out          bf16 [total_q][h][128];  lse_out fp32 [total_q][h] or NULL (natural
  *                log, as from gqla_combine).  Rows that belong to no sequence are left
  *                as they were.
@@ -327,7 +328,8 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
  * n_b > L_b, L_b beyond its page-table row) is reported (GQLA_ERR_DEVICE, info = b)
  * and its rows are left as they were; a page index outside the pool is reported the
  * same way and leaves that sequence's rows unspecified.  Cached rows past L_b may hold
- * anything, NaN too, and so may keys that a query does not see; values (V) of the L_b
+ * anything, NaN too, and so may keys that a query does not see; a NaN among the
+ * scores that a row sees makes the row and its LSE NaN; values (V) of the L_b
  * tokens are finite (one that is not reaches all rows of its query block of 4 (128 / G)
  * tokens, G = h/g, those before it too).
  * Precision: bf16 operands, scores, softmax and its sum in fp32, P rounded to bf16
