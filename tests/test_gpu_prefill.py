@@ -355,3 +355,25 @@ def test_prefill_nan_scores_reach_their_rows_only(shape, splits, what):
     keep = ~nan & ~torch.isnan(z)
     assert bool(((got.double() - out).abs() <= tol_o)[keep].all())
     assert bool(((lse.double() - z).abs() <= tol_l)[keep].all())
+
+
+def test_prefill_calls_at_once_on_two_streams():
+    """Two calls with buffers of their own, again and again at the same time: each the bits of its
+    call alone."""
+    from decode_attention_06_b200 import gqla
+    cases = [make(128, 8, [333, 1, 40], [0, 700, 129], seed=21), make(32, 8, [130, 5, 64], [300, 2000, 0], seed=22)]
+    sides = []
+    for c, splits in zip(cases, (37, -9)):
+        dims = gqla.make_dims(c["h"], c["g"])
+        kv = gqla.make_kv_index(c["table"], c["seqlens"], c["pages"])
+        want, want_lse, err = call(c, splits)
+        assert err[0] == 0
+        sides.append((c, dims, kv, gqla.PrefillBuffers(dims, c["q"].shape[0], splits), torch.cuda.Stream(), want, want_lse))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for c, dims, kv, bufs, stream, _, _ in sides:
+            gqla.prefill_step(dims, bufs, c["q"], c["starts"], kv, c["kv"], c["rope"], stream=stream)
+    torch.cuda.synchronize()
+    for _, _, _, bufs, _, want, want_lse in sides:
+        assert gqla.gqla_read_device_error(bufs.workspace)[0] == 0
+        assert torch.equal(bufs.out, want) and torch.equal(bufs.lse, want_lse)
