@@ -604,7 +604,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                             if (nq == 1 && q != ((t - pc.t0) & 1)) continue;
                             const bool fresh = t - pc.t0 == (nq == 1 ? q : 0);  // O_q starts here
                             bool ok = true;
-                            if (nq == 1 || q == 0) ok = mbar_wait(&v_full[st], (s / kPfStages) & 1, abort_flag);
+                            if (nq == 1 || q == 0) {
+                                const uint32_t parity = (s / kPfStages) & 1;
+                                // cleared by warp 3 of either CTA, or as the copies left it
+                                ok = t == pc.nt - 1 && pc.kv_end % kPfTile != 0
+                                         ? mbar_wait_cluster(&v_full[st], parity, abort_flag)
+                                         : mbar_wait(&v_full[st], parity, abort_flag);
+                            }
                             if (fresh) ok = ok && mbar_wait(&o_free[q], (on[q]++ & 1) ^ 1, abort_flag);
                             ok = ok && mbar_wait(&p_full[q], pn[q]++ & 1, abort_flag);
                             if (!ok) *abort_flag = 1;
@@ -628,7 +634,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
             // the rows past it (later tokens, or slots that hold no token and may hold NaN) meet
             // P = 0 in the product and are cleared so that 0 x NaN cannot enter it. V of such a
             // tile arrives on a barrier of this CTA, and this warp passes its bytes on to the
-            // barrier that the O issuer waits for.
+            // barrier that the O issuer waits for. That issuer reads shared memory of both CTAs, so
+            // what orders the cleared rows before its product has cluster scope on both sides
+            // (a fence here, the wait there); once per block, it costs nothing that shows.
             PfIter it(plan, list);
             PfPiece pc;
             PfMerge merge{0, 0, 0, 0};
@@ -653,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    __threadfence_block();
+                    fence_acq_rel_cluster();
                     mbar_complete_tx_remote(lead(&v_full[st]), kPfV);
                 }
             }

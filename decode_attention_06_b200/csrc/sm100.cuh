@@ -580,6 +580,11 @@ __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr
                  : "memory");
 }
 
+// Orders this thread's accesses, and those it has seen, at cluster scope: before a relaxed
+// operation on a peer's mbarrier it hands them to a thread that waits there with
+// mbar_wait_cluster.
+__device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
 // Complete `bytes` of the transaction count of an mbarrier of any CTA of the cluster, as a
 // copy that has landed does.
 __device__ __forceinline__ void mbar_complete_tx_remote(uint32_t cluster_addr, uint32_t bytes) {

@@ -377,3 +377,21 @@ def test_prefill_calls_at_once_on_two_streams():
     for _, _, _, bufs, _, want, want_lse in sides:
         assert gqla.gqla_read_device_error(bufs.workspace)[0] == 0
         assert torch.equal(bufs.out, want) and torch.equal(bufs.lse, want_lse)
+
+
+@pytest.mark.parametrize("h,g,splits", [(128, 8, 74), (128, 8, -40), (32, 8, -16)])
+def test_prefill_rows_past_the_keys_never_enter(h, g, splits):
+    """Blocks that end at every kind of place in a key tile (in the first page, which one CTA of the pair
+    clears, in the second, at its start), with NaN in the slots behind them: call after call the bits
+    that zeros there give."""
+    new = [1, 5, 33, 40, 17, 64, 3, 90]
+    ctx = [0, 59, 31, 89, 110, 65, 253, 166]  # ends 1, 64, 64, 129, 127, 129, 256, 256
+    ctx += [c + 1 for c in ctx] + [c + 70 for c in ctx]
+    zeros = make(h, g, new * 3, ctx, seed=31, tail=0.0)
+    nans = make(h, g, new * 3, ctx, seed=31)
+    want = call(zeros, splits)
+    check(zeros, want[0], want[1])
+    for _ in range(40):
+        out, lse, err = call(nans, splits)
+        assert err[0] == 0
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
