@@ -391,6 +391,10 @@ __global__ void __launch_bounds__(kPgThreads) extend_kernel(const PgPool p, cons
         for (int o = 16; o > 0; o >>= 1) limit = max(limit, __shfl_xor_sync(0xffffffffu, limit, o));
         for (int given = 0; given < limit;) {
             const int n = listed ? limit : collect_free(p, min(limit - given, kPgList), &cursor, list, part);
+            if (n == 0) {  // pages that were counted are gone: another call is taking them meanwhile
+                if (tid == 0) report_error(p.ws, GQLA_ERR_DEVICE, b0);
+                break;
+            }
             for (int k = tid; k < n; k += kPgThreads) {
                 const int r = given + k;
                 int lo = 0, hi = kPgThreads;  // the last sequence whose ranks start at or before r

@@ -384,7 +384,9 @@ int gqla_append_cache(const gqla_dims *dims, const void *rows, int64_t total_q, 
  * RoPE keys, of one layer or many): the table calls run once per step, the copies once
  * per layer.  New pages are the lowest free ones, in list order, so results do not
  * depend on timing.  Each call's first device-side error goes to its workspace; what is
- * in error is left out, the rest is done.
+ * in error is left out, the rest is done.  Calls on one pool must not overlap on the GPU,
+ * nor with calls that read its table and lengths (one stream, or events between streams):
+ * they would give the same pages twice.
  */
 typedef struct {
     int32_t *page_table;   /* device int32 [batch][max_pages_per_seq] */

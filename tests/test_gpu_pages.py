@@ -402,3 +402,24 @@ def test_extend_by_more_pages_than_32_bits_count():
     assert table[0, :pages].tolist() == [0, 1] + [-7] * (pages - 2) and bool((table[1:, :pages] == -7).all())
     st, info = gqla.gqla_read_device_error(ws)
     assert st == -5 and 1 <= info < batch
+
+
+@pytest.mark.parametrize("batch,room", [(700, 12000), (1024, 5300), (1500, 14000)])
+def test_extend_by_thousands_of_pages_from_a_fragmented_pool(batch, room):
+    """More pages for one group of 1024 sequences than the list in shared memory holds: given out in
+    several rounds from free pages that lie scattered, until the pool is full in the smaller pools."""
+    rng = random.Random(room)
+    ref = Pool(batch, 12, room)
+    grow = [rng.choice([0, 64, 200, 300]) for _ in range(batch)]
+    ref.extend(grow)
+    ref.free(rng.sample(range(batch), batch // 2))
+    for p in rng.sample([p for p, r in enumerate(ref.refs) if r == 0], 50):
+        ref.refs[p] = 1  # held by a table of another kind
+    g = Gpu(ref, caches=False)
+    for _ in range(2):
+        grow = [rng.choice([0, 64, 400, 500, 500]) for _ in range(batch)]
+        g.extend(grow)
+        bad = ref.extend(grow)
+        torch.cuda.synchronize()
+        g.same(ref)
+        g.error(bad)
