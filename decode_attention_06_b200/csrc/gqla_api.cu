@@ -1,5 +1,6 @@
 // gqla_api.cu -- the extern "C" entry points of libgqla (declared in
 // include/gqla.h): argument validation, then launches on the caller's stream.
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -63,6 +64,10 @@ namespace {
 
 constexpr size_t kWorkspaceBytes = 256;
 
+// The most pages that the cache calls can address (their num_slots is below 2^31), and the longest
+// table row that a 32-bit length can fill.
+constexpr int kMaxPoolPages = INT_MAX / kPage, kMaxRowPages = INT_MAX / kPage + 1;
+
 // gqla_plan_prefill, in the plan's cost units (about a microsecond): the shortest chunk that
 // a block is divided for, the merge's launch and run, and the most blocks that are walked.
 constexpr int64_t kMinChunk = 8, kMergeCost = 5, kMaxWalk = 4096;
@@ -111,6 +116,8 @@ int check_pool(const gqla_page_pool *p) {
     if (!p || !p->page_table || !p->seqlens || !p->page_refs) return GQLA_ERR_INVALID_ARG;
     if (p->batch <= 0 || p->max_pages_per_seq <= 0 || p->num_pages <= 0) return GQLA_ERR_INVALID_ARG;
     if (p->batch > 65535 || p->page_size != kPage) return GQLA_ERR_UNSUPPORTED;
+    // the kernels count pages, and 8192 beyond the last, in 32 bits
+    if (p->num_pages > kMaxPoolPages || p->max_pages_per_seq > kMaxRowPages) return GQLA_ERR_UNSUPPORTED;
     return GQLA_OK;
 }
 

@@ -393,9 +393,9 @@ typedef struct {
     int32_t *seqlens;      /* device int32 [batch]                    */
     int32_t *page_refs;    /* device int32 [num_pages]                */
     int batch;             /* 1..65535                                */
-    int max_pages_per_seq;
-    int page_size;         /* 64                                      */
-    int num_pages;
+    int max_pages_per_seq; /* up to 2^25     (GQLA_ERR_UNSUPPORTED beyond, */
+    int page_size;         /* 64                       as for the others) */
+    int num_pages;         /* below 2^25: num_slots of the caches < 2^31   */
 } gqla_page_pool;
 
 /*

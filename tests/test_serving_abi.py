@@ -169,3 +169,23 @@ def test_prefill_slots(lib):
     assert lib.gqla_prefill_slots(129) == 2 * 129 + 2
     assert lib.gqla_prefill_slots(1) == lib.gqla_prefill_slots(-7) == 0
     assert lib.gqla_prefill_slots(0) == lib.gqla_prefill_slots(65536) == lib.gqla_prefill_slots(-65536) == -1
+
+
+def test_pools_beyond_32_bit_page_counts_are_refused(lib):
+    """Scans step 8192 pages past the last, and a row past 2^25 pages cannot be filled: both in 32 bits."""
+    def calls(pages, width):
+        p = _pool(num_pages=pages)
+        p.max_pages_per_seq = width
+        P = ctypes.byref(p)
+        # calls with nothing to do, so that an accepted pool launches nothing
+        return (lib.gqla_fork_sequences(P, FAKE, 0, FAKE, *WS, None), lib.gqla_free_sequences(P, FAKE, 0, *WS, None))
+
+    most = (1 << 25) - 1
+    assert calls(most, 4) == calls(16, most + 1) == calls(most, most + 1) == (0, 0)
+    for pages, width in ((most + 1, 4), ((1 << 31) - 1, 4), ((1 << 31) - 8000, 4), (16, most + 2), (16, (1 << 31) - 1)):
+        assert calls(pages, width) == (-2, -2)
+        p = _pool(num_pages=pages)
+        p.max_pages_per_seq = width
+        P = ctypes.byref(p)
+        assert lib.gqla_extend_sequences(P, FAKE, *WS, None) == -2
+        assert lib.gqla_compact_pages(P, FAKE, FAKE, FAKE, FAKE, *WS, None) == -2
