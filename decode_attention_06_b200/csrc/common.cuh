@@ -53,7 +53,10 @@ __device__ __forceinline__ void report_error(void *ws, int code, int info) {
 // device-resident lengths; nothing is precomputed on the host.
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ int pages_of(int len) { return len > 0 ? (len + kPage - 1) / kPage : 0; }
+// (unsigned: a length may be 2^31 - 1)
+__device__ __forceinline__ int pages_of(int len) {
+    return len > 0 ? static_cast<int>((static_cast<uint32_t>(len) + kPage - 1) / kPage) : 0;
+}
 
 __device__ __forceinline__ int warp_incl_scan(int v) {
     const int lane = threadIdx.x & 31;

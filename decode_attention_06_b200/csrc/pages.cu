@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kPgThreads) extend_kernel(const PgPool p, cons
         if (b < p.batch) {
             const int L = p.lens[b], n = new_tokens[b];
             len = (int64_t)L + n;
-            grow = n > 0 && L >= 0 && len <= (int64_t)p.max_pages * kPage;
+            grow = n > 0 && L >= 0 && len <= min((int64_t)p.max_pages * kPage, (int64_t)INT_MAX);
             if (n != 0 && !grow) report_error(p.ws, GQLA_ERR_DEVICE, b);
             have = pages_of(L);
             add = grow ? (int)((len + kPage - 1) / kPage) - have : 0;

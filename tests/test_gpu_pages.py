@@ -423,3 +423,28 @@ def test_extend_by_thousands_of_pages_from_a_fragmented_pool(batch, room):
         torch.cuda.synchronize()
         g.same(ref)
         g.error(bad)
+
+
+def test_lengths_up_to_the_largest():
+    """2^31 - 1 tokens: the pages of such a length, its free and its compaction, and no growth past it."""
+    from decode_attention_06_b200 import gqla
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    most, width = (1 << 31) - 1, 1 << 25
+    table = torch.full((2, width), 3, dtype=torch.int32, device="cuda")
+    table[1, 0] = 2
+    lens, refs, ws = i32([most, 5]), i32([0, 0, 1, width, 0]), gqla.new_workspace()
+    pool = gqla.make_page_pool(table, lens, refs)
+    gqla.gqla_extend_sequences(pool, i32([1, 1]), ws)
+    torch.cuda.synchronize()
+    assert lens.tolist() == [most, 6] and refs.tolist() == [0, 0, 1, width, 0]
+    assert gqla.gqla_read_device_error(ws) == (-5, 0)
+    gqla.gqla_clear_device_error(ws)
+    pairs, counts = i32([[9, 9]] * 2), i32([0, 0])
+    gqla.gqla_compact_pages(pool, table, refs, pairs, counts, ws)
+    torch.cuda.synchronize()
+    assert counts.tolist() == [2, 2] and pairs.tolist() == [[2, 0], [3, 1]]
+    assert refs.tolist() == [1, width, 0, 0, 0] and bool((table[0] == 1).all()) and int(table[1, 0]) == 0
+    gqla.gqla_free_sequences(pool, i32([0]), ws)
+    torch.cuda.synchronize()
+    assert lens.tolist() == [0, 6] and refs.tolist() == [1, 0, 0, 0, 0]
+    assert gqla.gqla_read_device_error(ws)[0] == 0
