@@ -296,7 +296,7 @@ struct PfIter {
             o.ntok = min(4 * p.tile_tokens, n - first);
             o.pos0 = L - n + first;
             o.kv_end = o.pos0 + o.ntok;
-            o.nt = (int)((uint32_t)(o.kv_end + kPfTile - 1) / kPfTile);
+            o.nt = (int)(((uint32_t)o.kv_end + kPfTile - 1) / kPfTile);  // kv_end may be 2^31 - 1
             const int w = pf_weight(o.ntok, p.tile_tokens);
             o.t0 = t;
             o.t1 = p.whole ? o.nt : (int)min((int64_t)o.nt, (end - u0 + w - 1) >> (w - 1));  // w is 1 or 2
@@ -455,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                 struct Slots { int s0, s1; };
                 auto slots = [&](const PfPiece &pc, int t) -> Slots {
                     const int32_t *row = p.page_table + (int64_t)pc.b * p.max_pages;
-                    const int pg = 2 * t, pages = (pc.kv_end + kPage - 1) / kPage;
+                    const int pg = 2 * t, pages = pages_of(pc.kv_end);
                     const int a0 = row[pg], a1 = pg + 1 < pages ? row[pg + 1] : 0;
                     const bool ok0 = a0 >= 0 && a0 < p.num_pages, ok1 = a1 >= 0 && a1 < p.num_pages;
                     if (!ok0 || !ok1) report_error(p.ws, GQLA_ERR_DEVICE, pc.b);

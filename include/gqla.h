@@ -430,8 +430,8 @@ int gqla_fork_sequences(const gqla_page_pool *pool, const int32_t *forks, int nu
  * Extends every sequence by new_tokens[b] >= 0 tokens (device int32 [batch]): its pages
  * from the free ones, sequence after sequence, then its length.  A sequence whose pages
  * do not all fit (or whose row is too short, one past 2^31 - 1 tokens, or a negative
- * number) is reported (info = b) and unchanged, and once the free pages have run out so is every later one
- * that needs a page.
+ * number) is reported (info = b) and unchanged, and once the free pages have run out
+ * so is every later one that needs a page.
  */
 int gqla_extend_sequences(const gqla_page_pool *pool, const int32_t *new_tokens, void *workspace,
                           size_t workspace_bytes, gqla_stream_t stream);

@@ -395,3 +395,36 @@ def test_prefill_rows_past_the_keys_never_enter(h, g, splits):
         out, lse, err = call(nans, splits)
         assert err[0] == 0
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_prefill_length_of_31_bits():
+    """A sequence of 2^31 - 1 tokens over a few pages named again and again; its very last page is one of
+    its own, with a key that outweighs all others: the answer is that key's value."""
+    from decode_attention_06_b200 import gqla
+    most, width, pages = (1 << 31) - 1, 1 << 25, 5
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+    kv, rope, q = rnd(1, pages * 64, 256), rnd(pages * 64, 64) * 0.01, rnd(2, 16, 192)
+    table = (torch.arange(width, device="cuda", dtype=torch.int32) % 4).view(1, -1)
+    table[0, -1] = 4
+    # the last two tokens are the queries; scores of 1000 for key 2^31 - 3, -1000 for the very last one,
+    # a few units for the rest: 2^31 of them weigh e^(22 + 30 - 1000), nothing in float32
+    q[..., 128:] = 0
+    q[..., 128] = 100.0
+    rope[:, 0] = 0
+    rope[4 * 64 + 61, 0], rope[4 * 64 + 62, 0] = 144.0, -144.0
+    starts = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    idx = gqla.make_kv_index(table, torch.tensor([most], dtype=torch.int32, device="cuda"), pages)
+    dims = gqla.make_dims(16, 1)
+    bufs = gqla.PrefillBuffers(dims, 2, gqla.plan_prefill(dims, [2], [most]))
+    out, lse = gqla.prefill_step(dims, bufs, q, starts, idx, kv, rope)
+    torch.cuda.synchronize()
+    assert gqla.gqla_read_device_error(bufs.workspace)[0] == 0
+    k = torch.cat([kv[0, 4 * 64 + 61, :128], rope[4 * 64 + 61]]).double()
+    score = torch.einsum("nhd,d->nh", q.double(), k) * SCALE
+    assert bool((score > 900).all())
+    mag = torch.einsum("nhd,d->nh", q.double().abs(), k.abs()) * SCALE
+    assert bool(((lse.double() - score).abs() <= 192 * E * mag + 2.0 ** -20 + 2.0 ** -22 * score).all())
+    # P is 1 for that key (or a power of two off it by the score's rounding, the same in O and l), 0 elsewhere
+    v = kv[0, 4 * 64 + 61, 128:].double()
+    assert bool(((out.double() - v).abs() <= (2 * U + 2.0 ** -20) * v.abs()).all())
