@@ -55,9 +55,11 @@ constexpr int kPfThreads = 384;
 constexpr int kPfLaunchRegs = 168;
 constexpr int kPfIssueRegs = 72, kPfSoftmaxRegs = 216;
 static_assert(128 * kPfIssueRegs + 256 * kPfSoftmaxRegs <= kPfThreads * kPfLaunchRegs, "register split");
-// A row's base is looked at anew when a tile's sum is above 2^64 (or under a mask), and raised
-// if the maximum is more than 2^8 above it.
-constexpr float kPfRise = 18446744073709551616.0f, kPfRescaleLog2 = 8.0f;
+// A row's base is looked at anew when a tile's sum is above 2^16 (or under a mask), and raised
+// if the maximum is more than 2^8 above it. 128 scores that stay below that sum to 2^15 at most,
+// so a sum above 2^16 always raises the base. P is at most 2^16 then, l and the unnormalised O at
+// most 2^16 a tile (times max |V|): O stays below 2^128 for |V| up to 2^118 / L.
+constexpr float kPfRise = 65536.0f, kPfRescaleLog2 = 8.0f;
 
 constexpr int kPfBox = 64 * 128;          // one TMA box: 64 rows of 128 bytes
 constexpr int kPfK = 3 * kPfBox;          // a key tile's K in one CTA: its page's 64 keys x 192
@@ -723,7 +725,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfThreads, 1)
                     const bool masked = __any_sync(0xffffffffu, lim < kPfTile);
                     // P against the base so far, at once. The base of a row (its largest score when
                     // it was set, in log2 units) need not be its maximum: bf16 and fp32 have the
-                    // exponents for P up to 2^64, and P, O and l are all relative to it. It
+                    // exponents for P up to 2^16 (kPfRise), and P, O and l are all relative to it. It
                     // is set on a piece's first tile and under a mask, and again where a sum says
                     // that the scores rose too far above it (or that there was none yet, or that
                     // a score is NaN).

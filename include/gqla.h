@@ -331,7 +331,8 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
  * anything, NaN too, and so may keys that a query does not see; a NaN among the
  * scores that a row sees makes the row and its LSE NaN; values (V) of the L_b
  * tokens are finite (one that is not reaches all rows of its query block of 4 (128 / G)
- * tokens, G = h/g, those before it too).
+ * tokens, G = h/g, those before it too) and up to 2^118 / L_b (their sum is formed in
+ * fp32 before it is divided by that of the weights).
  * Precision: bf16 operands, scores, softmax and its sum in fp32, P rounded to bf16
  * (the tensor-core operand), O accumulated in fp32, one rounding to bf16.
  */

@@ -428,3 +428,24 @@ def test_prefill_length_of_31_bits():
     # P is 1 for that key (or a power of two off it by the score's rounding, the same in O and l), 0 elsewhere
     v = kv[0, 4 * 64 + 61, 128:].double()
     assert bool(((out.double() - v).abs() <= (2 * U + 2.0 ** -20) * v.abs()).all())
+
+
+@pytest.mark.parametrize("step", [5.0, 12.0, 70.0])
+@pytest.mark.parametrize("splits", [None, 1, -7, 23])
+@pytest.mark.parametrize("values", [0, 100])
+def test_prefill_scores_that_step_with_every_tile(step, splits, values):
+    """Scores that rise by `step` powers of two with every key tile in some rows, by half of that in
+    others, fall in others and stay level in the rest, side by side in a warp: bases that are raised
+    seldom, with every tile, or once the sum has grown over several; in blocks of two MMA tiles, in the
+    even and odd halves of blocks of one, and in pieces. And with values near 2^100, inside the range
+    that the header gives (2^118 / L)."""
+    c = make(128, 8, [50, 3, 16, 1], [900, 1300, 640, 2000], seed=17)
+    per_tile = step * math.log(2.0) / SCALE
+    for b, L in enumerate(c["lens"]):
+        c["rope"][c["slots"][b], 0] = (per_tile * (torch.arange(L, device="cuda") // 128)).to(torch.bfloat16)
+    kind = (torch.arange(c["q"].shape[0], device="cuda")[:, None] + torch.arange(128, device="cuda")) % 5
+    c["q"][..., 128] = torch.tensor([1.0, 0.0, -1.0, 0.5, 0.0], device="cuda")[kind].to(torch.bfloat16)
+    c["kv"][..., 128:] *= 2.0 ** values
+    out, lse, err = call(c, splits)
+    assert err[0] == 0
+    check(c, out, lse)
