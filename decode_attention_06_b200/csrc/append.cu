@@ -124,6 +124,8 @@ __device__ __forceinline__ void ap_copy(const ApParams &p, int64_t row0, int w, 
         const int64_t s = ap_slot(p, r + lane, lane < rows, true);
         if (!__all_sync(0xffffffffu, mbar_wait(bar, n & 1, abort_flag))) {
             *abort_flag = 1;
+            int dummy = 0;  // never leave with a copy in flight
+            mbar_wait(bar, n & 1, &dummy);
             break;
         }
         if (s >= 0) {
