@@ -72,6 +72,7 @@ constexpr int kMaxPoolPages = INT_MAX / kPage, kMaxRowPages = INT_MAX / kPage + 
 // a block is divided for, the merge's launch and run, and the most blocks that are walked.
 constexpr int64_t kMinChunk = 8, kMergeCost = 5, kMaxWalk = 4096;
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -96,6 +97,7 @@ int check_index(const gqla_kv_index *kv) {
     if (!kv || !kv->page_table || !kv->seqlens) return GQLA_ERR_INVALID_ARG;
     if (kv->batch <= 0 || kv->max_pages_per_seq <= 0 || kv->num_pages <= 0)
         return GQLA_ERR_INVALID_ARG;
+    if (!aligned4(kv->page_table) || !aligned4(kv->seqlens)) return GQLA_ERR_INVALID_ARG;
     if (kv->batch > 65535) return GQLA_ERR_UNSUPPORTED;
     if (kv->page_size != kPage) return GQLA_ERR_UNSUPPORTED;
     return GQLA_OK;
@@ -115,6 +117,7 @@ int check_ragged_dims(const gqla_dims *d) {
 int check_pool(const gqla_page_pool *p) {
     if (!p || !p->page_table || !p->seqlens || !p->page_refs) return GQLA_ERR_INVALID_ARG;
     if (p->batch <= 0 || p->max_pages_per_seq <= 0 || p->num_pages <= 0) return GQLA_ERR_INVALID_ARG;
+    if (!aligned4(p->page_table) || !aligned4(p->seqlens) || !aligned4(p->page_refs)) return GQLA_ERR_INVALID_ARG;
     if (p->batch > 65535 || p->page_size != kPage) return GQLA_ERR_UNSUPPORTED;
     // the kernels count pages, and 8192 beyond the last, in 32 bits
     if (p->num_pages > kMaxPoolPages || p->max_pages_per_seq > kMaxRowPages) return GQLA_ERR_UNSUPPORTED;
@@ -554,8 +557,8 @@ int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, cons
     if (!q_starts || !kv_expanded || !k_rope || (total_q > 0 && (!q || !out))) return GQLA_ERR_INVALID_ARG;
     const bool whole = num_splits <= 1;
     if (!whole && (!o_part || !lse_part)) return GQLA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(kv_expanded) || !aligned16(k_rope) || !aligned16(out) ||
-        (!whole && (!aligned16(o_part) || !aligned16(lse_part))))
+    if (!aligned16(q) || !aligned16(kv_expanded) || !aligned16(k_rope) || !aligned16(out) || !aligned4(q_starts) ||
+        !aligned4(lse_out) || (!whole && (!aligned16(o_part) || !aligned16(lse_part))))
         return GQLA_ERR_INVALID_ARG;
     if (num_slots != (int64_t)kv->num_pages * kv->page_size) return GQLA_ERR_INVALID_ARG;
     const int64_t most = ((int64_t)1 << 31) - 1;
@@ -579,7 +582,7 @@ int gqla_append_cache(const gqla_dims *dims, const void *rows, int64_t total_q, 
     if ((kv_expanded == nullptr) != (k_rope == nullptr)) return GQLA_ERR_INVALID_ARG;
     if (kv_expanded ? (!w_uk || !w_uv) : !latent_cache) return GQLA_ERR_INVALID_ARG;
     if (!aligned16(rows) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(latent_cache) ||
-        !aligned16(kv_expanded) || !aligned16(k_rope))
+        !aligned16(kv_expanded) || !aligned16(k_rope) || !aligned4(q_starts))
         return GQLA_ERR_INVALID_ARG;
     if (num_slots != (int64_t)kv->num_pages * kv->page_size) return GQLA_ERR_INVALID_ARG;
     const int64_t most = ((int64_t)1 << 31) - 1;
@@ -621,7 +624,7 @@ int gqla_extend_sequences(const gqla_page_pool *pool, const int32_t *new_tokens,
     int st = check_pool(pool);
     if (st != GQLA_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
-    if (!new_tokens) return GQLA_ERR_INVALID_ARG;
+    if (!new_tokens || !aligned4(new_tokens)) return GQLA_ERR_INVALID_ARG;
     return cuda_status(launch_extend(pool, new_tokens, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -630,7 +633,7 @@ int gqla_free_sequences(const gqla_page_pool *pool, const int32_t *seq_ids, int 
     int st = check_pool(pool);
     if (st != GQLA_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
-    if (num_ids < 0 || (num_ids > 0 && !seq_ids)) return GQLA_ERR_INVALID_ARG;
+    if (num_ids < 0 || (num_ids > 0 && !seq_ids) || !aligned4(seq_ids)) return GQLA_ERR_INVALID_ARG;
     if (num_ids > 65535) return GQLA_ERR_UNSUPPORTED;
     if (num_ids == 0) return GQLA_OK;
     return cuda_status(launch_free(pool, seq_ids, num_ids, workspace, reinterpret_cast<cudaStream_t>(stream)));
@@ -641,7 +644,9 @@ int gqla_compact_pages(const gqla_page_pool *pool, int32_t *page_table_out, int3
     int st = check_pool(pool);
     if (st != GQLA_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes)) != GQLA_OK) return st;
-    if (!page_table_out || !page_refs_out || !pairs || !counts || !aligned8(pairs)) return GQLA_ERR_INVALID_ARG;
+    if (!page_table_out || !page_refs_out || !pairs || !counts || !aligned8(pairs) || !aligned4(page_table_out) ||
+        !aligned4(page_refs_out) || !aligned4(counts))
+        return GQLA_ERR_INVALID_ARG;
     return cuda_status(launch_compact(pool, page_table_out, page_refs_out, pairs, counts, workspace,
                                       reinterpret_cast<cudaStream_t>(stream)));
 }

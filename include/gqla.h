@@ -19,7 +19,8 @@
  *
  * Conventions for every call:
  *  - All tensor arguments are DEVICE pointers owned by the caller, dense,
- *    row-major, 16-byte aligned.  Nothing is allocated, freed or copied to
+ *    row-major, 16-byte aligned (int32 tensors: by their type, pairs by 8
+ *    bytes).  Nothing is allocated, freed or copied to
  *    the host, and no call synchronises: work is enqueued on `stream`
  *    (NULL = the legacy default stream) and the call returns.
  *  - bf16 means IEEE bfloat16 (2 bytes).  "h" is dims->num_heads, "g" is

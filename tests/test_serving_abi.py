@@ -189,3 +189,33 @@ def test_pools_beyond_32_bit_page_counts_are_refused(lib):
         P = ctypes.byref(p)
         assert lib.gqla_extend_sequences(P, FAKE, *WS, None) == -2
         assert lib.gqla_compact_pages(P, FAKE, FAKE, FAKE, FAKE, *WS, None) == -2
+
+
+def test_index_pointers_off_their_type_are_refused(lib):
+    """An int32 or float address that is no multiple of 4 would fault in the kernel: refused first, by
+    calls with nothing to do (which an accepted pointer lets through), too."""
+    assert _prefill(lib, total=0) == _append(lib, total=0) == 0
+    assert _prefill(lib, total=0, starts=off(2)) == _append(lib, total=0, starts=off(1)) == -1
+    assert _prefill(lib, total=0, starts=off(4)) == _append(lib, total=0, starts=off(4)) == 0
+    d = _dims()
+    assert lib.gqla_prefill_gqa(ctypes.byref(d), FAKE, I64(0), FAKE, FAKE, FAKE, SLOTS, ctypes.byref(_kv()), -1, None, None,
+                                FAKE, off(2), *WS, None) == -1
+    for name in ("page_table", "seqlens"):
+        idx = _kv()
+        setattr(idx, name, off(3))
+        assert _prefill(lib, total=0, idx=idx) == _append(lib, total=0, idx=idx) == -1
+    for name in ("page_table", "seqlens", "page_refs"):
+        p = _pool()
+        setattr(p, name, off(2))
+        P = ctypes.byref(p)
+        assert lib.gqla_fork_sequences(P, FAKE, 0, FAKE, *WS, None) == -1
+        assert lib.gqla_free_sequences(P, FAKE, 0, *WS, None) == -1
+        assert lib.gqla_extend_sequences(P, FAKE, *WS, None) == -1
+        assert lib.gqla_compact_pages(P, FAKE, FAKE, FAKE, FAKE, *WS, None) == -1
+    P = ctypes.byref(_pool())
+    assert lib.gqla_free_sequences(P, off(2), 0, *WS, None) == -1
+    assert lib.gqla_extend_sequences(P, off(2), *WS, None) == -1
+    for i in range(4):
+        a = [FAKE] * 4
+        a[i] = off(2)
+        assert lib.gqla_compact_pages(P, *a, *WS, None) == -1
