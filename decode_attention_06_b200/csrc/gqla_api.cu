@@ -515,8 +515,8 @@ int gqla_plan_prefill(const gqla_dims *dims, const int32_t *new_tokens, const in
         *num_splits = -1;
         return GQLA_OK;
     }
-    // Divided: equal chunks, none below kMinChunk units (a piece of a block costs about as much
-    // as a whole one: its start, its end and its partials), then the merge.
+    // Divided: equal chunks, none below kMinChunk units, then the merge. (The piece that a cut adds
+    // to a chunk, with a start, an end and partials of its own, is not counted.)
     const int64_t div = std::max<int64_t>(1, std::min<int64_t>(max_splits, total / kMinChunk));
     const int64_t div_cost = pf_chunk(total, (int)div) + kMergeCost;
     // Whole blocks: the heaviest chunk, walked through where the blocks are few enough for their

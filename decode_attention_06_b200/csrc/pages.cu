@@ -81,7 +81,7 @@ struct CpParams {
     uint8_t *latent, *kv, *rope;
     void *ws;
     int64_t n, num_pages;
-    int groups, pieces, lat_pieces, kv_pieces, words;
+    int pieces, lat_pieces, kv_pieces, words;
 };
 
 __device__ __forceinline__ int ld_cluster_b32(uint32_t addr) {
@@ -566,7 +566,6 @@ cudaError_t launch_copy_pages(const int32_t *pairs, int64_t n, int num_pages, in
     p.ws = ws;
     p.n = n;
     p.num_pages = num_pages;
-    p.groups = num_groups;
     p.lat_pieces = latent ? kLatPieces : 0;
     p.kv_pieces = kv ? num_groups * kKvPieces : 0;
     p.pieces = p.lat_pieces + p.kv_pieces + (k_rope ? 1 : 0);

@@ -327,7 +327,8 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
  * Any number of groups, 1 <= h/g <= 128 (GQLA_ERR_UNSUPPORTED otherwise).  A
  * sequence whose numbers are inconsistent (descending or out-of-range q_starts,
  * n_b > L_b, L_b beyond its page-table row) is reported (GQLA_ERR_DEVICE, info = b)
- * and its rows are left as they were; a page index outside the pool is reported the
+ * and its rows are left as they were (rows that two other sequences then both claim,
+ * because q_starts descend between them, are unspecified); a page index outside the pool is reported the
  * same way and leaves that sequence's rows unspecified.  Cached rows past L_b may hold
  * anything, NaN too, and so may keys that a query does not see; a NaN among the
  * scores that a row sees makes the row and its LSE NaN; values (V) of the L_b
@@ -369,7 +370,8 @@ int gqla_plan_prefill(const gqla_dims *dims, const int32_t *new_tokens, const in
  *                 may be NULL too); at least one of the two caches is given
  * Accumulation and accuracy as for gqla_expand_cache_tc; latent rows and RoPE keys are
  * copied exactly.  Sequences with inconsistent numbers are reported and left out as by
- * gqla_prefill_gqa, and so are tokens whose page is outside the pool.  Two sequences
+ * gqla_prefill_gqa, and so are tokens whose page is outside the pool.  g <= 4096
+ * (GQLA_ERR_UNSUPPORTED beyond).  Two sequences
  * of the batch must not share the page of a new token (gqla_fork_sequences gives a
  * fork a page of its own for that).
  */
@@ -408,7 +410,7 @@ typedef struct {
  *           source or a page onto itself is skipped
  * A pair with a page outside the pool, one whose target another pair writes too, and
  * one whose source another pair writes are reported (GQLA_ERR_DEVICE, info = pair) and
- * left out.  num_pages <= 524288 (GQLA_ERR_UNSUPPORTED beyond).
+ * left out.  num_pages <= 524288, g <= 4096 (GQLA_ERR_UNSUPPORTED beyond).
  */
 int gqla_copy_pages(const gqla_dims *dims, const int32_t *pairs, int64_t num_pairs, int num_pages, void *latent_cache,
                     void *kv_expanded, void *k_rope, void *workspace, size_t workspace_bytes, gqla_stream_t stream);
@@ -423,7 +425,8 @@ int gqla_copy_pages(const gqla_dims *dims, const int32_t *pairs, int64_t num_pai
  *           be named any number of times.  num_forks <= 65535
  *   pairs   device int32 [num_forks][2], out
  * A fork that breaks these rules, or finds no free page, is reported (info = its index)
- * and its child stays empty.
+ * and its child stays empty.  A full page of the parent that is outside the pool is
+ * reported too; the child's row names it like the parent's.
  */
 int gqla_fork_sequences(const gqla_page_pool *pool, const int32_t *forks, int num_forks, int32_t *pairs,
                         void *workspace, size_t workspace_bytes, gqla_stream_t stream);
