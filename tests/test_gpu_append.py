@@ -145,3 +145,14 @@ def test_append_does_the_sequences_beside_starts_that_descend(at, value, skip):
         out, err = run(d, **what)
         assert err[0] == -5 and err[1] in skip
         check(c, out, skip=skip, **what)
+
+
+@pytest.mark.parametrize("g", [16, 20, 37, 40])
+@pytest.mark.parametrize("new,ctx", [([1], [200]), ([40, 3, 129], [0, 64, 61]), ([1500, 700], [10, 0])])
+def test_append_of_many_groups(g, new, ctx):
+    """One product to a pair as long as all fit on the SMs, several beyond; group counts that few powers
+    of two divide."""
+    c = make(g, new, ctx, seed=g, gap=2, h=2 * g)
+    out, err = run(c)
+    assert err[0] == 0
+    check(c, out)

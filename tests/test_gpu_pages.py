@@ -448,3 +448,25 @@ def test_lengths_up_to_the_largest():
     torch.cuda.synchronize()
     assert lens.tolist() == [0, 6] and refs.tolist() == [1, 0, 0, 0, 0]
     assert gqla.gqla_read_device_error(ws)[0] == 0
+
+
+def test_copy_pages_in_more_than_one_round():
+    """More pieces than the CTAs take in one round of 256 each (about 37900 on 148 SMs), with pairs that
+    are skipped or clash strewn among them, so that the rounds hold uneven counts."""
+    pages, groups, n = 2400, 8, 1100  # 42 pieces a pair
+    g = Gpu(Pool(1, 1, pages), groups)
+    rng = random.Random(77)
+    order = rng.sample(range(pages), 2 * n + 60)
+    good = [(order[2 * i], order[2 * i + 1]) for i in range(n)]
+    spare = order[2 * n:]
+    clash = [(spare[2 * i], spare[40 + i % 20]) for i in range(20)]  # targets named twice below
+    clash += [(spare[2 * i + 1], spare[40 + i % 20]) for i in range(20)]
+    listed = good + clash + [(-1, 3)] * 150 + [(7, 7)] * 100
+    rng.shuffle(listed)
+    want = copied((g.latent, g.kv, g.rope), groups, good)
+    for _ in range(2):
+        g.copy(torch.tensor(listed, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    g.error([i for i, p in enumerate(listed) if p in clash])
+    for got, exp in zip((g.latent, g.kv, g.rope), want):
+        assert torch.equal(got, exp)

@@ -449,3 +449,13 @@ def test_prefill_scores_that_step_with_every_tile(step, splits, values):
     out, lse, err = call(c, splits)
     assert err[0] == 0
     check(c, out, lse)
+
+
+@pytest.mark.parametrize("h,g", [(64, 16), (37, 37), (80, 20), (48, 2), (40, 1), (200, 2), (127, 1)])
+@pytest.mark.parametrize("splits", [None, 1, 26, -9])
+def test_prefill_of_other_head_layouts(h, g, splits):
+    """More groups than 8, and group sizes that leave rows of the tile unused (24, 40, 100, 127 heads)."""
+    c = make(h, g, [1, 6, 0, 45], [130, 250, 9, 71], seed=h, gap=2)
+    out, lse, err = call(c, splits)
+    assert err[0] == 0
+    check(c, out, lse)

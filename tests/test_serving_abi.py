@@ -219,3 +219,28 @@ def test_index_pointers_off_their_type_are_refused(lib):
         a = [FAKE] * 4
         a[i] = off(2)
         assert lib.gqla_compact_pages(P, *a, *WS, None) == -1
+
+
+def test_more_groups_than_the_grids_hold_are_refused(lib):
+    many = _dims(h=4097, g=4097)
+    assert _append(lib, d=many) == -2
+    assert lib.gqla_copy_pages(ctypes.byref(many), FAKE, I64(1), 16, FAKE, None, None, *WS, None) == -2
+    assert lib.gqla_copy_pages(ctypes.byref(_dims(h=4096, g=4096)), FAKE, I64(0), 16, FAKE, None, None, *WS, None) == 0
+
+
+def test_the_binding_refuses_an_index_of_another_device(monkeypatch):
+    import torch
+
+    from decode_attention_06_b200 import gqla
+    t = torch.zeros(2, dtype=torch.int32)
+    pool = gqla.gqla_page_pool(FAKE, FAKE, FAKE, 2, 4, 64, 16)
+    pool._keep, pool._device = (t,), 1
+    monkeypatch.setattr(gqla, "_current_device", lambda: 0)
+    for call in (lambda: gqla.gqla_fork_sequences(pool, t.view(1, 2), t.view(1, 2), t),
+                 lambda: gqla.gqla_extend_sequences(pool, t, t), lambda: gqla.gqla_free_sequences(pool, t, t),
+                 lambda: gqla.gqla_compact_pages(pool, t, t, t, t, t)):
+        with pytest.raises(ValueError, match="current device is cuda:0"):
+            call()
+    pool._device = -1  # tensors that share no device
+    with pytest.raises(ValueError, match="current device"):
+        gqla.gqla_free_sequences(pool, t, t)
