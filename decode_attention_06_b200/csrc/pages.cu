@@ -5,9 +5,11 @@
 // every run (reference counts change by integer atomics, whose order does not matter).
 //
 // The table calls are latency-bound, one launch each: 256 forks of sequences of 1500 tokens 9 us,
-// 288 sequences extended 6.8 us, a pool of 2048 pages compacted 10 us. Fork and compact run as
+// 288 sequences extended 6.8 us, a pool of 2048 pages compacted 11 us. Fork and compact run as
 // one cluster of eight CTAs, whose first CTA scans the reference counts while the others wait
-// at the cluster barrier, and which then rewrite the table rows together.
+// at the cluster barrier, and which then rewrite the table rows together. Of larger pools the scan
+// of one CTA shows: 20000 pages 27 us to compact and 10 us for 64 forks, 200000 pages 216 and 19 us;
+// extend, which stops where it has found enough, stays at 7 us.
 #include <limits.h>
 
 #include "common.cuh"

@@ -337,6 +337,8 @@ int gqla_combine_lead(const gqla_dims *dims, const gqla_kv_index *kv, int s_q, i
  * fp32 before it is divided by that of the weights).
  * Precision: bf16 operands, scores, softmax and its sum in fp32, P rounded to bf16
  * (the tensor-core operand), O accumulated in fp32, one rounding to bf16.
+ * Its longest device-side waits run out after about a minute: a call that keeps a CTA
+ * pair busy for longer may end with GQLA_ERR_TIMEOUT.  Cut such a prompt into chunks.
  */
 int gqla_prefill_gqa(const gqla_dims *dims, const void *q, int64_t total_q, const int32_t *q_starts,
                      const void *kv_expanded, const void *k_rope, int64_t num_slots, const gqla_kv_index *kv,
